@@ -43,12 +43,22 @@ namespace {
 // e4m3 caches: codes go to fp16 by one conversion instruction for two values
 // (exact), the products run on fp16 with q scaled by a power of two per row
 // (exact down to 2^-28 of the row's largest), the key's scale multiplies the
-// score.  The value's scale 2^e joins the weight, and the running maximum is
-// taken of score + e, so the fp16 weights stay in range whatever the scales:
+// score.  The value's scale 2^e joins the weight, and the running maximum m
+// is taken of score + e, so the fp16 weights stay in range whatever the scales:
 // the largest is at least 2^7 and at most 2^15, and fp16's subnormals are 2^-24
-// apart (a weight is off by 2^-11 of itself, or 2^-32 of the largest).  An e
-// below -85 counts as -85 there, which keeps the sum of weights, taken without
-// e, under 2^(15 + 85) a key.
+// apart (a weight is off by 2^-11 of itself, or 2^-32 of the largest).
+//
+// The weights of the sum l go without e.  While every e is within 60 of 0, one
+// exponential 2^(score - m) serves both: the sum's terms are at most 2^75, the
+// largest at least 2^-53, and what ends at 2^-126 matters to neither.  From the
+// first tile with an e beyond that (bf16 rows past 2^69, or all below 2^-51) a
+// warp's item is wide: l then has a maximum u of the scores alone and an
+// exponential of its own, the weight is 2^(score - m + e), and the output is
+// sum / l * 2^(m - u).  The first exponents beyond are found where the reference
+// is about to move, and send the tile to the wide form, so that the others pay a
+// comparison and some registers (16 sequences to 8K: 62 us with 12 rows, 86 with
+// 28, 90 with 64 of head_dim 64; one reference for all, wrong beyond: 57, 85, 86;
+// two exponentials for all: 62, 91, 104).
 
 constexpr int kKeys = 64;      // keys of a tile
 constexpr int kThreads = 128;  // of the four consumer warps
@@ -56,8 +66,8 @@ constexpr int kThreads = 128;  // of the four consumer warps
 // 1 e4m3: 269 us with 64 keys, 181 with 192, 174 with 320, 175 with 512).
 constexpr int kFixedKeys = 5 * kKeys;
 
-// NB: turned products, 8 NB rows; 0: 16-row tiles.
-template <int HD, int TYPE, int NB>
+// NB: turned products, 8 NB rows; 0: WM 16-row tiles.
+template <int HD, int TYPE, int NB, int WM = 0>
 struct RowsCfg {
   static constexpr bool B16 = TYPE == ARMT_CACHE_BF16;
   static constexpr int ROW = B16 ? HD * 2 : HD;       // bytes of a cached row
@@ -66,12 +76,13 @@ struct RowsCfg {
   static constexpr int POOL = kKeys * ROW;
   static constexpr int SCALES = B16 ? 0 : 2 * kKeys;
   static constexpr int STAGE = (2 * POOL + SCALES + 1023) / 1024 * 1024;
-  static constexpr int BLOCKS = HD == 64 || (NB == 1 && !B16) ? 3 : 2;  // resident on an SM (registers, mostly)
+  // resident on an SM: registers, mostly (64 rows over codes: 90 us, 100 with three blocks, whose sums spill)
+  static constexpr int BLOCKS = (HD == 64 && (B16 || WM != 4)) || (NB == 1 && !B16) ? 3 : 2;
   static constexpr int JOIN = 2 * 32 * 32 * 4;  // two warps' pieces of 32 values a lane
   static constexpr int QUERIES = NB * HD * 16;  // turned: the queries' fragments
   // as many buffers, up to 6, as those blocks find room for beside a KB that
   // each block costs, its static shared memory and a KB of alignment
-  static constexpr int ROOM = 233472 / BLOCKS - 1024 - (12 * HD + 512) - 1024 - JOIN - QUERIES;
+  static constexpr int ROOM = 233472 / BLOCKS - 1024 - (12 * HD + 768) - 1024 - JOIN - QUERIES;
   static constexpr int STAGES = ROOM / STAGE < 6 ? ROOM / STAGE : 6;
   static_assert(STAGES >= 2, "a buffer to fill beside the one in use");
   static constexpr int SMEM = 1024 + STAGES * STAGE + JOIN + QUERIES;
@@ -133,6 +144,26 @@ __device__ __forceinline__ void mma16816(float* d, const uint32_t* a, uint32_t b
         "{%0, %1, %2, %3};"
         : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
         : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+
+// Whether a value's scale byte is beyond what one reference serves; and the
+// exponent of a byte in the weights of a wide item: -inf for a scale of zero,
+// +inf for infinity.
+__device__ __forceinline__ bool wide_scale(uint32_t byte) { return byte - 67u > 120u; }
+__device__ __forceinline__ float scale_exponent(uint32_t byte) {
+  return byte == 0u ? -INFINITY : byte == 255u ? INFINITY : (float)((int)byte - 127);
+}
+
+// What a row's sum of products in reference m is multiplied by, one after the
+// other, for its output: 1 / l, l in reference u, and 2^(m - u) in two halves (it
+// may be 2^140).
+struct RowFactors {
+  float first, second;
+};
+__device__ __forceinline__ RowFactors row_factors(float l, float m, float u) {
+  const float inv = l == 0.f ? 0.f : 1.f / l;
+  const float half = m == u ? 1.f : fast_exp2(0.5f * (m - u));
+  return RowFactors{inv * half, half};
 }
 
 // Two e4m3 codes (low 16 bits) -> two fp16.
@@ -233,10 +264,10 @@ __device__ __forceinline__ void produce(const CUtensorMap& tm_k, const CUtensorM
 }
 
 template <int HD, int TYPE, int WM>
-__global__ void __launch_bounds__(kThreads + 32, RowsCfg<HD, TYPE, 0>::BLOCKS)
+__global__ void __launch_bounds__(kThreads + 32, RowsCfg<HD, TYPE, 0, WM>::BLOCKS)
     rows_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v, const PagedArgs a,
                 const PagedView p) {
-  using C = RowsCfg<HD, TYPE, 0>;
+  using C = RowsCfg<HD, TYPE, 0, WM>;
   constexpr int WN = 4 / WM;             // warps that share rows and split keys
   constexpr int KPW = kKeys / WN;        // keys of a tile for one warp
   constexpr int R = 16 * WM;             // rows of a query tile
@@ -248,6 +279,7 @@ __global__ void __launch_bounds__(kThreads + 32, RowsCfg<HD, TYPE, 0>::BLOCKS)
                                              ~static_cast<uintptr_t>(1023));
   __shared__ Poison bad[HD];
   __shared__ RowsShared<C> sh;
+  __shared__ float sum_ref[B16 ? 1 : 4][16];  // wide items: u of each warp's rows
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int wm = warp % WM, wn = warp / WM;
   const int r = lane >> 2, c = lane & 3;
@@ -278,11 +310,12 @@ __global__ void __launch_bounds__(kThreads + 32, RowsCfg<HD, TYPE, 0>::BLOCKS)
   int visible[2];  // keys this thread's two rows see
   int seen_min = 0, seen_max = 0;
   bool noted = false;  // this thread has written to `bad` for the query tile
+  bool wide = false;   // this warp's sums have two references (the same for all its lanes)
 
   // reads the rows of the query tile at `at`, and starts its sums
   auto start_item = [&]() {
     const int rows = at.n * a.plan.group;
-    noted = false;
+    noted = wide = false;
     int qrow[2];
     bool valid[2];
 #pragma unroll
@@ -346,8 +379,9 @@ __global__ void __launch_bounds__(kThreads + 32, RowsCfg<HD, TYPE, 0>::BLOCKS)
 
   // The tile in `stage`: scores, weights, and their product with the values.
   // `mask`: not every row sees all of it, or some of it has no page; what lies
-  // in such slots is taken out before it can touch a sum.
-  auto add_tile = [&](int stage, int k0, auto mask) {
+  // in such slots is taken out before it can touch a sum.  Not in the wide form
+  // and an exponent that wants it: false, and nothing done.
+  auto add_tile = [&](int stage, int k0, auto mask, auto wide_form) {
     const uint32_t sk = sbase + stage * C::STAGE, sv = sk + C::POOL;
     const int kw = wn * KPW;  // this warp's first key of the tile
     const uint32_t ok = mask() ? sh.with_page[stage] : 15u;
@@ -391,9 +425,11 @@ __global__ void __launch_bounds__(kThreads + 32, RowsCfg<HD, TYPE, 0>::BLOCKS)
       }
     }
     // to log2 units, masked
-    [[maybe_unused]] float ve[KPW / 8][2];  // e4m3: the value scale of this thread's keys
-    bool moves = false;  // a row's reference has to move (see turned_kernel)
+    [[maybe_unused]] float ve[KPW / 8][2];  // e4m3: the value scale (wide: its exponent) of this thread's keys
+    [[maybe_unused]] bool beyond = false;   // one of them wants the wide form
+    bool moves = wide_form();  // a row's reference has to move (see turned_kernel)
     float mx[2] = {-INFINITY, -INFINITY};
+    [[maybe_unused]] float uref[2];
 #pragma unroll
     for (int t = 0; t < KPW / 8; ++t) {
       [[maybe_unused]] float kf[2] = {1.f, 1.f}, ev[2] = {0.f, 0.f};
@@ -402,10 +438,12 @@ __global__ void __launch_bounds__(kThreads + 32, RowsCfg<HD, TYPE, 0>::BLOCKS)
         for (int i = 0; i < 2; ++i) {
           const uint32_t at_key = sk + 2 * C::POOL + kw + 8 * t + key_of(2 * c + i);
           uint32_t kbyte = lds_u8(at_key), vbyte = lds_u8(at_key + kKeys);
-          if (mask() && !(ok >> ((kw + 8 * t) >> 4) & 1u)) kbyte = vbyte = 0;
+          if (mask() && (k0 + kw + 8 * t + key_of(2 * c + i) >= seen_max || !(ok >> ((kw + 8 * t) >> 4) & 1u)))
+            kbyte = vbyte = 127;  // seen by no row: may be anything
           kf[i] = scale_of(kbyte);
-          ve[t][i] = scale_of(vbyte);
-          ev[i] = fmaxf((float)((int)vbyte - 127), -85.f);
+          ve[t][i] = wide_form() ? scale_exponent(vbyte) : scale_of(vbyte);
+          ev[i] = (float)((int)vbyte - 127);
+          beyond |= !wide_form() && wide_scale(vbyte);
         }
       }
 #pragma unroll
@@ -423,7 +461,8 @@ __global__ void __launch_bounds__(kThreads + 32, RowsCfg<HD, TYPE, 0>::BLOCKS)
     }
 #pragma unroll
     for (int h = 0; h < 2; ++h) moves |= mx[h] > m[h] + kRaise;
-    if (__any_sync(0xffffffffu, moves)) {
+    if (__any_sync(0xffffffffu, moves || beyond)) {
+      if (!B16 && !wide_form() && __any_sync(0xffffffffu, beyond)) return false;
       float corr[2];
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
@@ -431,8 +470,25 @@ __global__ void __launch_bounds__(kThreads + 32, RowsCfg<HD, TYPE, 0>::BLOCKS)
         mx[h] = fmaxf(mx[h], __shfl_xor_sync(0xffffffffu, mx[h], 2));
         const float next = fmaxf(m[h], mx[h] - kNominal), ref = next == -INFINITY ? 0.f : next;
         corr[h] = m[h] == next ? 1.f : fast_exp2(m[h] - ref);
+        if constexpr (wide_form()) {
+          const float from = wide ? sum_ref[warp][r + 8 * h] : m[h];
+          float up = from;
+#pragma unroll
+          for (int t = 0; t < KPW / 8; ++t) up = fmaxf(up, fmaxf(s[t][2 * h], s[t][2 * h + 1]));
+          up = fmaxf(up, __shfl_xor_sync(0xffffffffu, up, 1));
+          up = fmaxf(up, __shfl_xor_sync(0xffffffffu, up, 2));
+          l[h] *= from == up ? 1.f : fast_exp2(from - up);
+          uref[h] = up == -INFINITY ? 0.f : up;
+          __syncwarp();
+          if (c == 0) sum_ref[warp][r + 8 * h] = up;
+        } else {
+          l[h] *= corr[h];
+        }
         m[h] = next;
-        l[h] *= corr[h];
+      }
+      if constexpr (wide_form()) {
+        wide = true;
+        __syncwarp();
       }
 #pragma unroll
       for (int t = 0; t < NT; ++t) {
@@ -447,12 +503,16 @@ __global__ void __launch_bounds__(kThreads + 32, RowsCfg<HD, TYPE, 0>::BLOCKS)
     for (int t = 0; t < KPW / 8; ++t) {
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
-        const float w = fast_exp2(s[t][i] - ref[i >> 1]);
-        l[i >> 1] += w;
-        s[t][i] = w;
-        if constexpr (!B16) {
-          s[t][i] = w * ve[t][i & 1];
-          if (mask() && w == 0.f) s[t][i] = 0.f;  // a masked slot's scale byte may say infinity
+        if constexpr (wide_form()) {
+          const float x = s[t][i];
+          l[i >> 1] += fast_exp2(x - uref[i >> 1]);
+          s[t][i] = fast_exp2(x - ref[i >> 1] + ve[t][i & 1]);
+          if (x == -INFINITY) s[t][i] = 0.f;  // a masked slot's scale byte may say infinity
+        } else {
+          const float w = fast_exp2(s[t][i] - ref[i >> 1]);
+          l[i >> 1] += w;
+          s[t][i] = w;
+          if constexpr (!B16) s[t][i] = w * ve[t][i & 1];
         }
       }
     }
@@ -534,6 +594,7 @@ __global__ void __launch_bounds__(kThreads + 32, RowsCfg<HD, TYPE, 0>::BLOCKS)
         }
       }
     }
+    return true;
   };
 
   // column of o[t][0] (and o[t][2]); o[t][1] is `next` further
@@ -542,8 +603,10 @@ __global__ void __launch_bounds__(kThreads + 32, RowsCfg<HD, TYPE, 0>::BLOCKS)
 
   // joins the warps' sums and writes the query tile's rows, or its partial sums
   auto finish_item = [&](bool whole, int slot) {
+    [[maybe_unused]] float u[2];  // codes: the reference of l
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
+      if constexpr (!B16) u[h] = wide ? sum_ref[warp][r + 8 * h] : m[h];
       l[h] += __shfl_xor_sync(0xffffffffu, l[h], 1);
       l[h] += __shfl_xor_sync(0xffffffffu, l[h], 2);
     }
@@ -554,8 +617,10 @@ __global__ void __launch_bounds__(kThreads + 32, RowsCfg<HD, TYPE, 0>::BLOCKS)
       const int box = (wn % half) * WM + wm;  // at most two boxes
       float f_mine[2] = {1.f, 1.f}, f_other[2] = {1.f, 1.f};
       consumers_sync();
-      if (gives)
+      if (gives) {
         *reinterpret_cast<float4*>(join + (box * 32 + lane) * 4) = make_float4(m[0], m[1], l[0], l[1]);
+        if constexpr (!B16) *reinterpret_cast<float2*>(join + 256 + (box * 32 + lane) * 2) = make_float2(u[0], u[1]);
+      }
       consumers_sync();
       if (takes) {
         const float4 y = *reinterpret_cast<const float4*>(join + (box * 32 + lane) * 4);
@@ -565,7 +630,14 @@ __global__ void __launch_bounds__(kThreads + 32, RowsCfg<HD, TYPE, 0>::BLOCKS)
           const float top = fmaxf(m[h], om[h]), ref = top == -INFINITY ? 0.f : top;
           f_mine[h] = fast_exp2(m[h] - ref);
           f_other[h] = fast_exp2(om[h] - ref);
-          l[h] = l[h] * f_mine[h] + ol[h] * f_other[h];
+          if constexpr (B16) {
+            l[h] = l[h] * f_mine[h] + ol[h] * f_other[h];
+          } else {
+            const float ou = join[256 + (box * 32 + lane) * 2 + h];
+            const float up = fmaxf(u[h], ou), uref = up == -INFINITY ? 0.f : up;
+            l[h] = l[h] * fast_exp2(u[h] - uref) + ol[h] * fast_exp2(ou - uref);
+            u[h] = up;
+          }
           m[h] = top;
         }
       }
@@ -605,21 +677,25 @@ __global__ void __launch_bounds__(kThreads + 32, RowsCfg<HD, TYPE, 0>::BLOCKS)
         if (whole) {
           const int tok = row / a.plan.group, head = at.head * a.plan.group + row % a.plan.group;
           bf16* dst = a.out + (long long)(at.row0 + tok) * a.out_stride + head * HD;
-          const float inv = l[h] == 0.f ? 0.f : 1.f / l[h];
           if constexpr (B16) {
+            const float inv = l[h] == 0.f ? 0.f : 1.f / l[h];
 #pragma unroll
             for (int t = 0; t < NT; ++t)
               *reinterpret_cast<uint32_t*>(dst + 8 * t + 2 * c) = pack_bf16x2(o[t][2 * h] * inv, o[t][2 * h + 1] * inv);
           } else {
+            const RowFactors f = row_factors(l[h], m[h], u[h]);
+            auto two = [&](float x, float y) {
+              return pack_bf16x2(x * f.first * f.second, y * f.first * f.second);
+            };
 #pragma unroll
             for (int j = 0; j < 2; ++j)
 #pragma unroll
               for (int t = 0; t < NT; t += 8) {
                 uint4 y;
-                y.x = pack_bf16x2(o[t][2 * h + j] * inv, o[t + 1][2 * h + j] * inv);
-                y.y = pack_bf16x2(o[t + 2][2 * h + j] * inv, o[t + 3][2 * h + j] * inv);
-                y.z = pack_bf16x2(o[t + 4][2 * h + j] * inv, o[t + 5][2 * h + j] * inv);
-                y.w = pack_bf16x2(o[t + 6][2 * h + j] * inv, o[t + 7][2 * h + j] * inv);
+                y.x = two(o[t][2 * h + j], o[t + 1][2 * h + j]);
+                y.y = two(o[t + 2][2 * h + j], o[t + 3][2 * h + j]);
+                y.z = two(o[t + 4][2 * h + j], o[t + 5][2 * h + j]);
+                y.w = two(o[t + 6][2 * h + j], o[t + 7][2 * h + j]);
                 *reinterpret_cast<uint4*>(dst + 2 * NT * c + j * NT + t) = y;
               }
           }
@@ -631,7 +707,12 @@ __global__ void __launch_bounds__(kThreads + 32, RowsCfg<HD, TYPE, 0>::BLOCKS)
             dst[column(t)] = o[t][2 * h];
             dst[column(t) + kNext] = o[t][2 * h + 1];
           }
-          if (c == 0) a.part_ml[idx] = make_float2(m[h], l[h]);
+          if (c == 0) {
+            if constexpr (B16)
+              a.part_ml[idx] = make_float2(m[h], l[h]);
+            else
+              reinterpret_cast<float4*>(a.part_ml)[idx] = make_float4(m[h], u[h], l[h], 0.f);
+          }
         }
       }
     }
@@ -655,7 +736,13 @@ __global__ void __launch_bounds__(kThreads + 32, RowsCfg<HD, TYPE, 0>::BLOCKS)
       const int k0 = (at.tile + j) * kKeys;
       if (got && k0 < seen_max) {  // some row sees the tile
         const bool all = k0 + kKeys <= seen_min && sh.with_page[stage] == 15u;
-        all ? add_tile(stage, k0, std::false_type()) : add_tile(stage, k0, std::true_type());
+        const std::false_type no;
+        const std::true_type yes;
+        if constexpr (B16) {
+          all ? add_tile(stage, k0, no, no) : add_tile(stage, k0, yes, no);
+        } else if (wide || !(all ? add_tile(stage, k0, no, no) : add_tile(stage, k0, yes, no))) {
+          add_tile(stage, k0, yes, yes);
+        }
       }
       __syncwarp();
       if (lane == 0) mbar_arrive(&sh.empty[stage]);
@@ -690,7 +777,10 @@ __global__ void __launch_bounds__(kThreads + 32, RowsCfg<HD, TYPE, NB>::BLOCKS)
                                              ~static_cast<uintptr_t>(1023));
   __shared__ Poison bad[HD];
   __shared__ RowsShared<C> sh;
+  // (read where they are needed: registers are short)
   __shared__ float scale_of_row[R];
+  __shared__ int visible_to_row[R];
+  __shared__ float sum_ref[B16 ? 1 : 4][R];  // as in rows_kernel
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int r = lane >> 2, c = lane & 3;
   const uint32_t sbase = smem_u32(smem);
@@ -712,19 +802,19 @@ __global__ void __launch_bounds__(kThreads + 32, RowsCfg<HD, TYPE, NB>::BLOCKS)
   PlanCursor at = range.first;
   // o[nb][t][i]: rows 8 nb + 2c + (i & 1), a value column for t and i >> 1
   float o[NB][KS][4];
-  float m[NB][2], l[NB][2], row_scale[NB][2];
-  int visible[NB][2];
+  float m[NB][2], l[NB][2];
   int seen_min = 0, seen_max = 0;
-  bool noted = false;
+  bool noted = false, wide = false;
 
   auto start_item = [&]() {
     const int rows = at.n * a.plan.group;
-    noted = false;
+    noted = wide = false;
     seen_min = plan_visible(at, at.qt * R / a.plan.group);
     seen_max = plan_visible(at, min(rows - 1, at.qt * R + R - 1) / a.plan.group);
     if (warp < NB) {  // this warp lays out the queries of 8 rows, a lane those of row r
       const int row = at.qt * R + 8 * warp + r, tok = row / a.plan.group;
       const bool valid = row < rows;
+      if (c == 0) visible_to_row[8 * warp + r] = valid ? plan_visible(at, tok) : 0;
       const bf16* q = a.q + (long long)(at.row0 + tok) * a.q_stride + (at.head * a.plan.group + row % a.plan.group) * HD;
       uint2 w[KS];
 #pragma unroll
@@ -764,9 +854,6 @@ __global__ void __launch_bounds__(kThreads + 32, RowsCfg<HD, TYPE, NB>::BLOCKS)
     for (int nb = 0; nb < NB; ++nb) {
 #pragma unroll
       for (int j = 0; j < 2; ++j) {
-        const int row = at.qt * R + 8 * nb + 2 * c + j;
-        visible[nb][j] = row < rows ? plan_visible(at, row / a.plan.group) : 0;
-        row_scale[nb][j] = B16 ? a.scale_log2 : scale_of_row[8 * nb + 2 * c + j];
         m[nb][j] = -INFINITY;
         l[nb][j] = 0.f;
       }
@@ -779,8 +866,8 @@ __global__ void __launch_bounds__(kThreads + 32, RowsCfg<HD, TYPE, NB>::BLOCKS)
   auto column = [&](int t, int i) { return B16 ? 16 * t + r + 8 * (i >> 1) : NC * r + 2 * t + (i >> 1); };
 
   // The tile in `stage`: this warp's 16 keys.  A thread's scores are of keys
-  // key0 and key0 + 8.  `mask` as in rows_kernel.
-  auto add_tile = [&](int stage, int k0, auto mask) {
+  // key0 and key0 + 8.  `mask`, `wide_form` and what is returned as in rows_kernel.
+  auto add_tile = [&](int stage, int k0, auto mask, auto wide_form) {
     const uint32_t sk = sbase + stage * C::STAGE, sv = sk + C::POOL;
     const int kw = warp * 16;
     const bool paged = !mask() || (sh.with_page[stage] >> warp & 1u);
@@ -824,35 +911,40 @@ __global__ void __launch_bounds__(kThreads + 32, RowsCfg<HD, TYPE, NB>::BLOCKS)
       }
     }
     [[maybe_unused]] float kf[2] = {1.f, 1.f}, vf[2] = {1.f, 1.f}, ev[2] = {0.f, 0.f};
+    [[maybe_unused]] bool beyond = false;
     if constexpr (!B16) {
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
         const uint32_t at_key = sk + 2 * C::POOL + key0 + 8 * h;
-        const uint32_t kbyte = paged ? lds_u8(at_key) : 0u, vbyte = paged ? lds_u8(at_key + kKeys) : 0u;
+        const bool held = !mask() || (paged && k0 + key0 + 8 * h < seen_max);  // (else its bytes may be anything)
+        const uint32_t kbyte = held ? lds_u8(at_key) : 127u, vbyte = held ? lds_u8(at_key + kKeys) : 127u;
         kf[h] = scale_of(kbyte);
-        vf[h] = scale_of(vbyte);
-        ev[h] = fmaxf((float)((int)vbyte - 127), -85.f);
+        vf[h] = wide_form() ? scale_exponent(vbyte) : scale_of(vbyte);
+        ev[h] = (float)((int)vbyte - 127);
+        beyond |= !wide_form() && wide_scale(vbyte);
       }
     }
     // scores in log2 units, and whether a row's reference has to move: only
     // when a weight would pass 2^8 times its nominal largest (1, or 2^7 over
     // codes, whose fp16 weights end at 2^16), which spares most tiles the
     // shuffles and the rescaling
-    bool moves = false;
+    bool moves = wide_form() || beyond;
 #pragma unroll
     for (int nb = 0; nb < NB; ++nb) {
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
         const int h = i >> 1, j = i & 1;  // key, row
-        float x = s[nb][i] * row_scale[nb][j];
+        float x = s[nb][i] * (B16 ? a.scale_log2 : scale_of_row[8 * nb + 2 * c + j]);
         if constexpr (!B16) x *= kf[h];
-        if (mask() && (k0 + key0 + 8 * h >= visible[nb][j] || !paged)) x = -INFINITY;
+        if (mask() && (k0 + key0 + 8 * h >= visible_to_row[8 * nb + 2 * c + j] || !paged)) x = -INFINITY;
         s[nb][i] = x;
         if constexpr (!B16) x += ev[h];
         moves |= x > m[nb][j] + kRaise;
       }
     }
+    [[maybe_unused]] float uref[NB][2];
     if (__any_sync(0xffffffffu, moves)) {
+      if (!B16 && !wide_form() && __any_sync(0xffffffffu, beyond)) return false;
 #pragma unroll
       for (int nb = 0; nb < NB; ++nb) {
         float corr[2];
@@ -863,13 +955,28 @@ __global__ void __launch_bounds__(kThreads + 32, RowsCfg<HD, TYPE, NB>::BLOCKS)
           for (int d = 4; d < 32; d <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, d));
           const float next = fmaxf(m[nb][j], mx - kNominal), ref = next == -INFINITY ? 0.f : next;
           corr[j] = m[nb][j] == next ? 1.f : fast_exp2(m[nb][j] - ref);
+          if constexpr (wide_form()) {
+            const float from = wide ? sum_ref[warp][8 * nb + 2 * c + j] : m[nb][j];
+            float up = fmaxf(from, fmaxf(s[nb][j], s[nb][2 + j]));
+#pragma unroll
+            for (int d = 4; d < 32; d <<= 1) up = fmaxf(up, __shfl_xor_sync(0xffffffffu, up, d));
+            l[nb][j] *= from == up ? 1.f : fast_exp2(from - up);
+            uref[nb][j] = up == -INFINITY ? 0.f : up;
+            __syncwarp();
+            if (r == 0) sum_ref[warp][8 * nb + 2 * c + j] = up;
+          } else {
+            l[nb][j] *= corr[j];
+          }
           m[nb][j] = next;
-          l[nb][j] *= corr[j];
         }
 #pragma unroll
         for (int t = 0; t < KS; ++t)
 #pragma unroll
           for (int i = 0; i < 4; ++i) o[nb][t][i] *= corr[i & 1];
+      }
+      if constexpr (wide_form()) {
+        wide = true;
+        __syncwarp();
       }
     }
     uint32_t w[NB][2];  // weights of 8 keys by 8 rows each, transposed into B fragments
@@ -880,11 +987,15 @@ __global__ void __launch_bounds__(kThreads + 32, RowsCfg<HD, TYPE, NB>::BLOCKS)
         float e[2];
 #pragma unroll
         for (int j = 0; j < 2; ++j) {
-          e[j] = fast_exp2(s[nb][2 * h + j] - (m[nb][j] == -INFINITY ? 0.f : m[nb][j]));
-          l[nb][j] += e[j];
-          if constexpr (!B16) {
-            const float x = e[j] * vf[h];
-            e[j] = mask() && e[j] == 0.f ? 0.f : x;  // a masked slot's scale byte may say infinity
+          const float x = s[nb][2 * h + j], above = x - (m[nb][j] == -INFINITY ? 0.f : m[nb][j]);
+          if constexpr (wide_form()) {
+            l[nb][j] += fast_exp2(x - uref[nb][j]);
+            e[j] = fast_exp2(above + vf[h]);
+            if (x == -INFINITY) e[j] = 0.f;  // a masked slot's scale byte may say infinity
+          } else {
+            e[j] = fast_exp2(above);
+            l[nb][j] += e[j];
+            if constexpr (!B16) e[j] *= vf[h];
           }
         }
         const uint32_t rows_of_key = pack2<Op>(e[0], e[1]);
@@ -941,6 +1052,7 @@ __global__ void __launch_bounds__(kThreads + 32, RowsCfg<HD, TYPE, NB>::BLOCKS)
 #pragma unroll
       for (int nb = 0; nb < NB; ++nb) mma16816<TYPE>(o[nb][t], v, w[nb][0], w[nb][1]);
     }
+    return true;
   };
 
   // Joins the four warps' sums and writes the query tile's rows, or its
@@ -949,13 +1061,19 @@ __global__ void __launch_bounds__(kThreads + 32, RowsCfg<HD, TYPE, NB>::BLOCKS)
   // adding up one of the four and writing it.
   auto finish_item = [&](bool whole, int slot) {
     float2* stats = reinterpret_cast<float2*>(join);  // [warp][row] reference, sum
+    [[maybe_unused]] float* refs = join + 8 * R;      // [warp][row] codes: the sum's reference
+    [[maybe_unused]] float u[NB][2];
 #pragma unroll
     for (int nb = 0; nb < NB; ++nb)
 #pragma unroll
       for (int j = 0; j < 2; ++j) {
 #pragma unroll
         for (int d = 4; d < 32; d <<= 1) l[nb][j] += __shfl_xor_sync(0xffffffffu, l[nb][j], d);
-        if (r == 0) stats[warp * R + 8 * nb + 2 * c + j] = make_float2(m[nb][j], l[nb][j]);
+        if (r == 0) {
+          const int row = 8 * nb + 2 * c + j;
+          stats[warp * R + row] = make_float2(m[nb][j], l[nb][j]);
+          if constexpr (!B16) refs[warp * R + row] = wide ? sum_ref[warp][row] : m[nb][j];
+        }
       }
     const bool poisoned = consumers_any(noted);  // every warp has noted its non-finite values, and read the queries
 #pragma unroll
@@ -972,8 +1090,21 @@ __global__ void __launch_bounds__(kThreads + 32, RowsCfg<HD, TYPE, NB>::BLOCKS)
         }
         const float ref = top == -INFINITY ? 0.f : top;
         l[nb][j] = 0.f;
+        if constexpr (B16) {
 #pragma unroll
-        for (int k = 0; k < 4; ++k) l[nb][j] += st[k].y * fast_exp2(st[k].x - ref);
+          for (int k = 0; k < 4; ++k) l[nb][j] += st[k].y * fast_exp2(st[k].x - ref);
+        } else {
+          float of[4];
+          u[nb][j] = -INFINITY;
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            of[k] = refs[k * R + 8 * nb + 2 * c + j];
+            u[nb][j] = fmaxf(u[nb][j], of[k]);
+          }
+          const float uref = u[nb][j] == -INFINITY ? 0.f : u[nb][j];
+#pragma unroll
+          for (int k = 0; k < 4; ++k) l[nb][j] += st[k].y * fast_exp2(of[k] - uref);
+        }
         own[j] = fast_exp2(m[nb][j] - ref);
         m[nb][j] = top;
       }
@@ -989,7 +1120,9 @@ __global__ void __launch_bounds__(kThreads + 32, RowsCfg<HD, TYPE, NB>::BLOCKS)
     };
 #pragma unroll
     for (int nb = 0; nb < NB; ++nb) {
-      const float inv[2] = {l[nb][0] == 0.f ? 0.f : 1.f / l[nb][0], l[nb][1] == 0.f ? 0.f : 1.f / l[nb][1]};
+      RowFactors f[2];
+#pragma unroll
+      for (int j = 0; j < 2; ++j) f[j] = row_factors(l[nb][j], m[nb][j], B16 ? m[nb][j] : u[nb][j]);
 #pragma unroll
       for (int t0 = 0; t0 < KS; t0 += 4) {
         consumers_sync();  // the statistics, or the tiles before, have been read
@@ -1005,7 +1138,9 @@ __global__ void __launch_bounds__(kThreads + 32, RowsCfg<HD, TYPE, NB>::BLOCKS)
           y[i] = 0.f;
 #pragma unroll
           for (int k = 0; k < 4; ++k) y[i] += join[(k * 16 + 4 * warp + i) * 32 + lane];
-          if (poisoned) y[i] += poison_of(bad[column(t, i)], visible[nb][i & 1]);
+          if (poisoned) y[i] += poison_of(bad[column(t, i)], visible_to_row[8 * nb + 2 * c + (i & 1)]);
+          if (whole) y[i] *= f[i & 1].first;
+          if (whole && !B16) y[i] *= f[i & 1].second;
         }
         if (whole && B16) {
           // columns r (and r + 8) of rows 2c, 2c + 1 -> row r, columns 2c, 2c + 1
@@ -1013,7 +1148,7 @@ __global__ void __launch_bounds__(kThreads + 32, RowsCfg<HD, TYPE, NB>::BLOCKS)
           bf16* dst = out_of(min(row, rows - 1)) + 16 * t + 2 * c;
 #pragma unroll
           for (int h = 0; h < 2; ++h) {
-            uint32_t z = pack_bf16x2(y[2 * h] * inv[0], y[2 * h + 1] * inv[1]);
+            uint32_t z = pack_bf16x2(y[2 * h], y[2 * h + 1]);
             asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(z) : "r"(z));
             if (row < rows) *reinterpret_cast<uint32_t*>(dst + 8 * h) = z;
           }
@@ -1024,7 +1159,7 @@ __global__ void __launch_bounds__(kThreads + 32, RowsCfg<HD, TYPE, NB>::BLOCKS)
           const int lr = 8 * nb + 2 * c + j, row = at.qt * R + lr;
           if (row >= rows) continue;
           if (whole) {
-            *reinterpret_cast<uint32_t*>(out_of(row) + column(t, 0)) = pack_bf16x2(y[j] * inv[j], y[2 + j] * inv[j]);
+            *reinterpret_cast<uint32_t*>(out_of(row) + column(t, 0)) = pack_bf16x2(y[j], y[2 + j]);
           } else {
             float* dst = a.part + (((long long)blockIdx.x * 2 + slot) * R + lr) * HD;
             dst[column(t, 0)] = y[j];
@@ -1036,8 +1171,12 @@ __global__ void __launch_bounds__(kThreads + 32, RowsCfg<HD, TYPE, NB>::BLOCKS)
 #pragma unroll
         for (int j = 0; j < 2; ++j) {
           const int lr = 8 * nb + 2 * c + j;
-          if (at.qt * R + lr < rows)
-            a.part_ml[((long long)blockIdx.x * 2 + slot) * R + lr] = make_float2(m[nb][j], l[nb][j]);
+          if (at.qt * R + lr >= rows) continue;
+          const long long idx = ((long long)blockIdx.x * 2 + slot) * R + lr;
+          if constexpr (B16)
+            a.part_ml[idx] = make_float2(m[nb][j], l[nb][j]);
+          else
+            reinterpret_cast<float4*>(a.part_ml)[idx] = make_float4(m[nb][j], u[nb][j], l[nb][j], 0.f);
         }
       }
     }
@@ -1058,8 +1197,14 @@ __global__ void __launch_bounds__(kThreads + 32, RowsCfg<HD, TYPE, NB>::BLOCKS)
           0xffffffffu, mbar_wait_bounded(&sh.full[stage], phase, err, DEV_TIMEOUT_FULL, a.wp.limit_ns));
       const int k0 = (at.tile + j) * kKeys;
       if (got && k0 < seen_max) {  // some row sees the tile
-        k0 + kKeys <= seen_min && sh.with_page[stage] == 15u ? add_tile(stage, k0, std::false_type())
-                                                             : add_tile(stage, k0, std::true_type());
+        const bool all = k0 + kKeys <= seen_min && sh.with_page[stage] == 15u;
+        const std::false_type no;
+        const std::true_type yes;
+        if constexpr (B16) {
+          all ? add_tile(stage, k0, no, no) : add_tile(stage, k0, yes, no);
+        } else if (wide || !(all ? add_tile(stage, k0, no, no) : add_tile(stage, k0, yes, no))) {
+          add_tile(stage, k0, yes, yes);
+        }
       }
       __syncwarp();
       if (lane == 0) mbar_arrive(&sh.empty[stage]);
@@ -1077,13 +1222,15 @@ __global__ void __launch_bounds__(kThreads + 32, RowsCfg<HD, TYPE, NB>::BLOCKS)
 // it a block.  The parts of a row are dealt to 8 or 16 groups of threads, each
 // thread taking 4 columns of 4 rows at a time, so that an item cut into many
 // parts is a few loads deep; the groups' sums meet in shared memory in group
-// order, so the order of all additions is fixed.
+// order, so the order of all additions is fixed.  TWO: the parts of an e4m3
+// cache's few-row kernels, whose sums of weights have a reference of their own.
 constexpr int kJoinRows = 16;
-template <int HD>
+template <int HD, bool TWO>
 __global__ void __launch_bounds__(256) join_kernel(const PagedArgs a, const PagedView p) {
   constexpr int COLS = HD / 4, GROUPS = 256 / COLS, DEEP = 4;
   __shared__ float4 sums[GROUPS][DEEP][COLS];
   __shared__ float2 stats[GROUPS][DEEP];  // reference, sum of weights
+  __shared__ float refs[TWO ? GROUPS : 1][DEEP];  // the sum's reference
   // every block waits, also those with nothing to do: this kernel's end then
   // says that both have ended
   asm volatile("griddepcontrol.wait;" ::: "memory");
@@ -1100,20 +1247,28 @@ __global__ void __launch_bounds__(256) join_kernel(const PagedArgs a, const Page
   const int col = threadIdx.x % COLS, grp = threadIdx.x / COLS;
   for (int base = row0; base < row1; base += DEEP) {
     float top[DEEP], l[DEEP];
+    [[maybe_unused]] float u[DEEP];
     float4 s[DEEP];
 #pragma unroll
     for (int d = 0; d < DEEP; ++d) {
-      top[d] = -INFINITY;
+      top[d] = u[d] = -INFINITY;
       l[d] = 0.f;
       s[d] = make_float4(0.f, 0.f, 0.f, 0.f);
     }
     for (int k = i - 1 + grp; k <= last; k += GROUPS) {
       float2 ml[DEEP];
+      [[maybe_unused]] float part_u[DEEP];
       float4 v[DEEP];
 #pragma unroll
       for (int d = 0; d < DEEP; ++d) {
         const long long idx = ((long long)k * 2 + (k == i - 1 ? 1 : 0)) * R + min(base + d, row1 - 1);
-        ml[d] = a.part_ml[idx];
+        if constexpr (TWO) {
+          const float4 st = reinterpret_cast<const float4*>(a.part_ml)[idx];
+          ml[d] = make_float2(st.x, st.z);
+          part_u[d] = st.y;
+        } else {
+          ml[d] = a.part_ml[idx];
+        }
         v[d] = *reinterpret_cast<const float4*>(a.part + idx * HD + 4 * col);
         if (ml[d].x == -INFINITY) v[d] = make_float4(0.f, 0.f, 0.f, 0.f);  // no sum there, perhaps nothing written
       }
@@ -1122,7 +1277,13 @@ __global__ void __launch_bounds__(256) join_kernel(const PagedArgs a, const Page
         const float m = fmaxf(top[d], ml[d].x), ref = m == -INFINITY ? 0.f : m;
         const float f0 = fast_exp2(top[d] - ref), f1 = fast_exp2(ml[d].x - ref);
         top[d] = m;
-        l[d] = l[d] * f0 + ml[d].y * f1;
+        if constexpr (TWO) {
+          const float up = fmaxf(u[d], part_u[d]), uref = up == -INFINITY ? 0.f : up;
+          l[d] = l[d] * fast_exp2(u[d] - uref) + ml[d].y * fast_exp2(part_u[d] - uref);
+          u[d] = up;
+        } else {
+          l[d] = l[d] * f0 + ml[d].y * f1;
+        }
         s[d].x = s[d].x * f0 + v[d].x * f1;
         s[d].y = s[d].y * f0 + v[d].y * f1;
         s[d].z = s[d].z * f0 + v[d].z * f1;
@@ -1134,6 +1295,7 @@ __global__ void __launch_bounds__(256) join_kernel(const PagedArgs a, const Page
     for (int d = 0; d < DEEP; ++d) {
       sums[grp][d][col] = s[d];
       if (col == 0) stats[grp][d] = make_float2(top[d], l[d]);
+      if (TWO && col == 0) refs[grp][d] = u[d];
     }
     __syncthreads();
     if (grp < DEEP && base + grp < row1) {
@@ -1141,20 +1303,32 @@ __global__ void __launch_bounds__(256) join_kernel(const PagedArgs a, const Page
 #pragma unroll
       for (int g = 0; g < GROUPS; ++g) m = fmaxf(m, stats[g][grp].x);
       const float ref = m == -INFINITY ? 0.f : m;
+      [[maybe_unused]] float up = -INFINITY, uref = 0.f;
+      if constexpr (TWO) {
+#pragma unroll
+        for (int g = 0; g < GROUPS; ++g) up = fmaxf(up, refs[g][grp]);
+        uref = up == -INFINITY ? 0.f : up;
+      }
       float o[4] = {0.f, 0.f, 0.f, 0.f}, sum = 0.f;
 #pragma unroll
       for (int g = 0; g < GROUPS; ++g) {
         const float2 st = stats[g][grp];
         const float4 v = sums[g][grp][col];
         const float f = fast_exp2(st.x - ref);
-        sum += f * st.y;
+        sum += st.y * (TWO ? fast_exp2(refs[TWO ? g : 0][grp] - uref) : f);
         o[0] += f * v.x, o[1] += f * v.y, o[2] += f * v.z, o[3] += f * v.w;
       }
-      const float inv = sum == 0.f ? 0.f : 1.f / sum;
+      const RowFactors f = row_factors(sum, m, TWO ? up : m);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) o[i] *= f.first;
+      if constexpr (TWO) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) o[i] *= f.second;
+      }
       const int row = at.qt * R + base + grp;
       const int tok = row / a.plan.group, head = at.head * a.plan.group + row % a.plan.group;
       bf16* dst = a.out + (long long)(at.row0 + tok) * a.out_stride + head * HD + 4 * col;
-      *reinterpret_cast<uint2*>(dst) = make_uint2(pack_bf16x2(o[0] * inv, o[1] * inv), pack_bf16x2(o[2] * inv, o[3] * inv));
+      *reinterpret_cast<uint2*>(dst) = make_uint2(pack_bf16x2(o[0], o[1]), pack_bf16x2(o[2], o[3]));
     }
   }
 }
@@ -1172,13 +1346,13 @@ armt_status launch_few(Kernel kernel, DeviceOnce& once, const PagedArgs& a, cons
     return refuse(ARMT_ERR_CUDA, "cuTensorMapEncodeTiled failed");
   kernel<<<a.plan.blocks, kThreads + 32, C::SMEM, st>>>(tm_k, tm_v, a, p);
   cudaError_t e = cudaGetLastError();
-  if (e == cudaSuccess) e = launch_join(a, p, cache.head_dim, st);
+  if (e == cudaSuccess) e = launch_join(a, p, cache.head_dim, !C::B16, st);
   return launch_status(e, "paged attention");
 }
 template <int HD, int TYPE, int WM>
 armt_status launch_rows(const PagedArgs& a, const PagedView& p, const armt_kv_cache& cache, cudaStream_t st) {
   static DeviceOnce once;
-  return launch_few<RowsCfg<HD, TYPE, 0>>(rows_kernel<HD, TYPE, WM>, once, a, p, cache, st);
+  return launch_few<RowsCfg<HD, TYPE, 0, WM>>(rows_kernel<HD, TYPE, WM>, once, a, p, cache, st);
 }
 template <int HD, int TYPE, int NB>
 armt_status launch_turned(const PagedArgs& a, const PagedView& p, const armt_kv_cache& cache, cudaStream_t st) {
@@ -1197,7 +1371,8 @@ armt_status launch_shape(int rows, const PagedArgs& a, const PagedView& p, const
 }
 template <int HD, int TYPE>
 int few_blocks(int rows) {
-  return rows == 8 ? RowsCfg<HD, TYPE, 1>::BLOCKS : RowsCfg<HD, TYPE, 0>::BLOCKS;
+  if (rows <= 16) return rows == 8 ? RowsCfg<HD, TYPE, 1>::BLOCKS : RowsCfg<HD, TYPE, 2>::BLOCKS;
+  return rows == 32 ? RowsCfg<HD, TYPE, 0, 2>::BLOCKS : RowsCfg<HD, TYPE, 0, 4>::BLOCKS;
 }
 
 // How a call is cut up: rows of a query tile, and blocks.  Both depend on
@@ -1224,7 +1399,7 @@ Shape shape_of(const armt_kv_cache& c, const armt_paged_batch& b, int group, int
     per_sm = c.head_dim == 64 ? (b16 ? few_blocks<64, ARMT_CACHE_BF16>(s.rows) : few_blocks<64, ARMT_CACHE_E4M3>(s.rows))
                               : (b16 ? few_blocks<128, ARMT_CACHE_BF16>(s.rows) : few_blocks<128, ARMT_CACHE_E4M3>(s.rows));
   s.blocks = per_sm * sms;
-  s.bytes = (int64_t)s.blocks * (2 * s.rows * (c.head_dim + 2) * 4 + (int64_t)sizeof(PlanRange));
+  s.bytes = (int64_t)s.blocks * (2 * s.rows * (c.head_dim + 4) * 4 + (int64_t)sizeof(PlanRange));
   return s;
 }
 
@@ -1243,7 +1418,7 @@ armt_status check_attention(const armt_kv_cache* cache, const armt_paged_batch* 
 
 }  // namespace
 
-cudaError_t launch_join(const PagedArgs& a, const PagedView& p, int head_dim, cudaStream_t st) {
+cudaError_t launch_join(const PagedArgs& a, const PagedView& p, int head_dim, bool two, cudaStream_t st) {
   if (a.plan.blocks < 2) return cudaSuccess;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)a.plan.blocks - 1, (unsigned)((a.plan.rows + kJoinRows - 1) / kJoinRows));
@@ -1254,8 +1429,8 @@ cudaError_t launch_join(const PagedArgs& a, const PagedView& p, int head_dim, cu
   at[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = at;
   cfg.numAttrs = 1;
-  return head_dim == 64 ? cudaLaunchKernelEx(&cfg, join_kernel<64>, a, p)
-                        : cudaLaunchKernelEx(&cfg, join_kernel<128>, a, p);
+  if (two) return cudaLaunchKernelEx(&cfg, head_dim == 64 ? join_kernel<64, true> : join_kernel<128, true>, a, p);
+  return cudaLaunchKernelEx(&cfg, head_dim == 64 ? join_kernel<64, false> : join_kernel<128, false>, a, p);
 }
 
 // Waits that gave up in the attention's kernels on the current device since the
@@ -1325,7 +1500,7 @@ extern "C" ARMT_API armt_status armt_paged_attention_bf16(const void* q, int64_t
     a.device = dev;
     a.part = static_cast<float*>(workspace);
     a.part_ml = reinterpret_cast<float2*>(a.part + (int64_t)shape.blocks * 2 * a.plan.rows * cache->head_dim);
-    a.plans = reinterpret_cast<PlanRange*>(a.part_ml + (int64_t)shape.blocks * 2 * a.plan.rows);
+    a.plans = reinterpret_cast<PlanRange*>(a.part_ml + (int64_t)shape.blocks * 4 * a.plan.rows);
     const PagedView p = paged_view(*cache, *batch);
     cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
     if (shape.tiles) return launch_tiles(a, p, *cache, n_q_heads, st);

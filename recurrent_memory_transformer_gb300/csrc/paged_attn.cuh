@@ -12,8 +12,8 @@ struct PagedArgs {
   long long q_stride, out_stride;
   float scale_log2;
   PagedPlan plan;
-  float* part;  // [block][2][plan.rows][head_dim], then their (reference, sum) pairs
-  float2* part_ml;
+  float* part;  // [block][2][plan.rows][head_dim], then the (reference, sum) of each row,
+  float2* part_ml;  // or (reference, the sum's reference, sum, -) from the few-row kernels over codes
   PlanRange* plans;  // [block]: what each block found for itself, for the joining kernel
   WaitPolicy wp;
   int device;
@@ -65,8 +65,9 @@ inline bool encode_pool(CUtensorMap* map, const void* pool, const armt_kv_cache&
 }
 
 // Launches the kernel that adds up the parts, as the dependent of the kernel
-// launched before it on the stream (which lets it in early).
-cudaError_t launch_join(const PagedArgs& a, const PagedView& p, int head_dim, cudaStream_t st);
+// launched before it on the stream (which lets it in early).  `two`: the parts
+// have two references.
+cudaError_t launch_join(const PagedArgs& a, const PagedView& p, int head_dim, bool two, cudaStream_t st);
 
 // The tensor-core kernel for many query rows (paged_tiles.cu): its query
 // tile's rows for a group of `group` heads, and its launch.

@@ -719,7 +719,7 @@ armt_status launch(const PagedArgs& a, const PagedView& p, const armt_kv_cache& 
     return refuse(ARMT_ERR_CUDA, "cuTensorMapEncodeTiled failed");
   tiles_kernel<HD, TYPE><<<a.plan.blocks, C::THREADS, C::SMEM, st>>>(tm_q, tm_k, tm_v, a, p, slot_tokens);
   cudaError_t e = cudaGetLastError();
-  if (e == cudaSuccess) e = launch_join(a, p, HD, st);
+  if (e == cudaSuccess) e = launch_join(a, p, HD, false, st);
   return launch_status(e, "paged attention");
 }
 
