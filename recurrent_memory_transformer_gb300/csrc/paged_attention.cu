@@ -155,13 +155,14 @@ __device__ __forceinline__ float scale_exponent(uint32_t byte) {
 }
 
 // What a row's sum of products in reference m is multiplied by, one after the
-// other, for its output: 1 / l, l in reference u, and 2^(m - u) in two halves (it
-// may be 2^140).
+// other, for its output: 1 / l, l in reference u (without weights: `empty`), and
+// 2^(m - u) in two halves (it may be 2^140).
 struct RowFactors {
   float first, second;
 };
-__device__ __forceinline__ RowFactors row_factors(float l, float m, float u) {
-  const float inv = l == 0.f ? 0.f : 1.f / l;
+template <typename Empty>
+__device__ __forceinline__ RowFactors row_factors(float l, float m, float u, Empty empty) {
+  const float inv = l == 0.f ? empty() : 1.f / l;
   const float half = m == u ? 1.f : fast_exp2(0.5f * (m - u));
   return RowFactors{inv * half, half};
 }
@@ -678,12 +679,12 @@ __global__ void __launch_bounds__(kThreads + 32, RowsCfg<HD, TYPE, 0, WM>::BLOCK
           const int tok = row / a.plan.group, head = at.head * a.plan.group + row % a.plan.group;
           bf16* dst = a.out + (long long)(at.row0 + tok) * a.out_stride + head * HD;
           if constexpr (B16) {
-            const float inv = l[h] == 0.f ? 0.f : 1.f / l[h];
+            const float inv = l[h] == 0.f ? empty_row(p, at.b, visible[h]) : 1.f / l[h];
 #pragma unroll
             for (int t = 0; t < NT; ++t)
               *reinterpret_cast<uint32_t*>(dst + 8 * t + 2 * c) = pack_bf16x2(o[t][2 * h] * inv, o[t][2 * h + 1] * inv);
           } else {
-            const RowFactors f = row_factors(l[h], m[h], u[h]);
+            const RowFactors f = row_factors(l[h], m[h], u[h], [&] { return empty_row(p, at.b, visible[h]); });
             auto two = [&](float x, float y) {
               return pack_bf16x2(x * f.first * f.second, y * f.first * f.second);
             };
@@ -1122,7 +1123,9 @@ __global__ void __launch_bounds__(kThreads + 32, RowsCfg<HD, TYPE, NB>::BLOCKS)
     for (int nb = 0; nb < NB; ++nb) {
       RowFactors f[2];
 #pragma unroll
-      for (int j = 0; j < 2; ++j) f[j] = row_factors(l[nb][j], m[nb][j], B16 ? m[nb][j] : u[nb][j]);
+      for (int j = 0; j < 2; ++j)
+        f[j] = row_factors(l[nb][j], m[nb][j], B16 ? m[nb][j] : u[nb][j],
+                           [&] { return whole ? empty_row(p, at.b, visible_to_row[8 * nb + 2 * c + j]) : 0.f; });
 #pragma unroll
       for (int t0 = 0; t0 < KS; t0 += 4) {
         consumers_sync();  // the statistics, or the tiles before, have been read
@@ -1226,7 +1229,7 @@ __global__ void __launch_bounds__(kThreads + 32, RowsCfg<HD, TYPE, NB>::BLOCKS)
 // cache's few-row kernels, whose sums of weights have a reference of their own.
 constexpr int kJoinRows = 16;
 template <int HD, bool TWO>
-__global__ void __launch_bounds__(256) join_kernel(const PagedArgs a, const PagedView p) {
+__global__ void __launch_bounds__(256, TWO ? 3 : 4) join_kernel(const PagedArgs a, const PagedView p) {
   constexpr int COLS = HD / 4, GROUPS = 256 / COLS, DEEP = 4;
   __shared__ float4 sums[GROUPS][DEEP][COLS];
   __shared__ float2 stats[GROUPS][DEEP];  // reference, sum of weights
@@ -1270,7 +1273,6 @@ __global__ void __launch_bounds__(256) join_kernel(const PagedArgs a, const Page
           ml[d] = a.part_ml[idx];
         }
         v[d] = *reinterpret_cast<const float4*>(a.part + idx * HD + 4 * col);
-        if (ml[d].x == -INFINITY) v[d] = make_float4(0.f, 0.f, 0.f, 0.f);  // no sum there, perhaps nothing written
       }
 #pragma unroll
       for (int d = 0; d < DEEP; ++d) {
@@ -1318,15 +1320,16 @@ __global__ void __launch_bounds__(256) join_kernel(const PagedArgs a, const Page
         sum += st.y * (TWO ? fast_exp2(refs[TWO ? g : 0][grp] - uref) : f);
         o[0] += f * v.x, o[1] += f * v.y, o[2] += f * v.z, o[3] += f * v.w;
       }
-      const RowFactors f = row_factors(sum, m, TWO ? up : m);
+      const int row = at.qt * R + base + grp;
+      const int tok = row / a.plan.group, head = at.head * a.plan.group + row % a.plan.group;
+      const RowFactors f =
+          row_factors(sum, m, TWO ? up : m, [&] { return empty_row(p, at.b, plan_visible(at, tok)); });
 #pragma unroll
       for (int i = 0; i < 4; ++i) o[i] *= f.first;
       if constexpr (TWO) {
 #pragma unroll
         for (int i = 0; i < 4; ++i) o[i] *= f.second;
       }
-      const int row = at.qt * R + base + grp;
-      const int tok = row / a.plan.group, head = at.head * a.plan.group + row % a.plan.group;
       bf16* dst = a.out + (long long)(at.row0 + tok) * a.out_stride + head * HD + 4 * col;
       *reinterpret_cast<uint2*>(dst) = make_uint2(pack_bf16x2(o[0], o[1]), pack_bf16x2(o[2], o[3]));
     }

@@ -48,6 +48,17 @@ __device__ __forceinline__ float poison_of(const Poison& t, int visible) {
   return v;
 }
 
+// What stands for 1 / (sum of weights) in a row whose weights are all zero: 0 if
+// none of the keys it could see has a page, so that it attends to nothing; NaN if
+// one has, whose scores are then all -inf: softmax is 0 / 0 there.  (Rare, and
+// over at the first page that is there.)
+__device__ __forceinline__ float empty_row(const PagedView& p, int b, int visible) {
+#pragma unroll 1
+  for (long long pos = 0; pos < visible; pos += 1ll << p.page_shift)
+    if (paged_page(p, b, pos) >= 0) return NAN;
+  return 0.f;
+}
+
 // Tensor map of a pool: rows of head_dim elements, page_size of them, a page
 // of one head after another; boxes of the rows that a tile of `keys` has in
 // one page, 128 bytes (64 for 64-byte rows) wide and swizzled over that width.

@@ -521,7 +521,11 @@ __global__ void __launch_bounds__(TileCfg<HD, TYPE>::THREADS, 1)
       const long long part =
           ((long long)blockIdx.x * 2 + (at.tile == 0 ? 1 : 0)) * a.plan.rows + (s * slot_tokens * a.plan.group + r);
       if (count == 0) {
-        if (valid) a.part_ml[part] = make_float2(-INFINITY, 0.f);
+        if (valid) {
+          a.part_ml[part] = make_float2(-INFINITY, 0.f);
+          for (int i = 0; i < HD; i += 4)
+            *reinterpret_cast<float4*>(a.part + part * HD + i) = make_float4(0.f, 0.f, 0.f, 0.f);
+        }
         continue;
       }
       const int seen_min = plan_visible(at, (long long)at.qt * 2 * slot_tokens);
@@ -634,7 +638,7 @@ __global__ void __launch_bounds__(TileCfg<HD, TYPE>::THREADS, 1)
       if (got && ok) {
         tc_fence_after();
         const bool poisoned = bar.any_bad != 0;
-        const float inv = l == 0.f ? 0.f : 1.f / l;
+        const float inv = l != 0.f ? 1.f / l : whole ? empty_row(p, at.b, visible) : 0.f;
         bf16* dst = a.out + (long long)(at.row0 + tok) * a.out_stride +
                     (at.head * a.plan.group + r % a.plan.group) * HD;
 #pragma unroll 1
@@ -645,7 +649,7 @@ __global__ void __launch_bounds__(TileCfg<HD, TYPE>::THREADS, 1)
           float o[32];
 #pragma unroll
           for (int i = 0; i < 32; ++i) {
-            o[i] = l == 0.f ? 0.f : __uint_as_float(x[i]);  // a row that saw nothing
+            o[i] = __uint_as_float(x[i]);
             if (poisoned) o[i] += poison_of(bad[32 * q + i], visible);
           }
           if (!valid) continue;

@@ -114,3 +114,84 @@ def test_many_small_weights_beside_a_large_one(hd, new, exponent):
     out = s.attend(q, scale=scale)
     s.check(q, out, scale=scale)
     assert ((out.double() * 2.0 ** -exponent)[..., 0] - 0.375).abs().max().item() < 2.0 ** -8
+
+
+# new rows for each kernel over a bf16 cache, then over an e4m3 one (4 heads a kv head)
+BOTH = [("bf16", 64, 1), ("bf16", 128, 3), ("bf16", 128, 7), ("bf16", 64, 12), ("bf16", 128, 40), ("bf16", 64, 40)] + \
+    [("e4m3", hd, n) for hd, n in ROWS if hd == 64 or n != 8]
+
+
+def minus_infinity(s, b, positions):
+    """Makes the scores of sequence b's keys at `positions` -inf, for queries of 1 in column 0 and 0 elsewhere."""
+    pos = np.array(positions)
+    page, slot = (torch.from_numpy(x).long().cuda() for x in (s.table[b, pos // s.page], pos % s.page))
+    if s.type == B.CACHE_BF16:
+        s.cache.k[page, :, slot, 0] = -math.inf
+    else:                                                    # -1 times infinity
+        s.cache.k.view(torch.uint8)[page, :, slot] = 0xB8
+        s.cache.k_scale[page, :, slot] = 255
+
+
+def first_column(s):
+    q = torch.zeros(s.n_rows, 4 * s.hkv, s.hd, dtype=torch.bfloat16, device="cuda")
+    q[..., 0] = 1.0
+    if s.type == B.CACHE_E4M3:
+        q[..., 1:] = 0.5                                     # (0 times infinity would be NaN)
+    return q
+
+
+@pytest.mark.parametrize("kv", [150, 20000])
+@pytest.mark.parametrize("type_,hd,new", BOTH)
+def test_a_row_whose_scores_are_all_minus_infinity(type_, hd, new, kv):
+    """0 / 0: NaN.  A row that attends to nothing, in the same call, stays zero, and other sequences are not touched."""
+    s = Wide(type_, 1, hd, 16, [new, 1, new, new], [kv, 33, 90, 40], seed=3)
+    s.table[2] = -1                                          # its pages are gone
+    s.batch = s.make_batch()
+    minus_infinity(s, 0, range(kv))
+    minus_infinity(s, 3, range(40))
+    s.k, s.v = s.k.copy(), s.v.copy()
+    for b, n in ((0, kv), (3, 40)):
+        for pos in range(n):
+            s.k[s.table[b, pos // 16], :, pos % 16] = 0.0
+            s.k[s.table[b, pos // 16], :, pos % 16, 0] = -math.inf
+    q = first_column(s)
+    out = s.attend(q)
+    first, other, gone, last = out.split([new, 1, new, new])
+    assert first.isnan().all() and last.isnan().all()
+    assert (gone == 0).all() and not other.isnan().any()
+    # the definition says the same (in the plain form's columns: the others of q times 0)
+    p = q.clone()
+    if type_ == "e4m3":
+        p[..., 1:] = 0
+        p[new] = q[new]
+    s.check(p, out)
+
+
+@pytest.mark.parametrize("kv", [200, 20000])
+@pytest.mark.parametrize("type_,hd,new", BOTH)
+def test_some_keys_at_minus_infinity_have_no_weight(type_, hd, new, kv):
+    """The front of a context at -inf, alone in the first part of one that is split."""
+    s = Wide(type_, 1, hd, 16, [new, 2], [kv, 70], seed=3)
+    front = range(kv - new - 40)
+    minus_infinity(s, 0, front)
+    q = first_column(s)
+    got = s.attend(q)
+    assert not got.isnan().any()
+    # the plain form with -1,000 in their place, which leaves them e^-100 and keeps the check's bound on scores
+    if type_ == "bf16":
+        s.refresh()
+    for pos in front:
+        at = s.table[0, pos // 16], slice(None), pos % 16
+        s.k[at] = 0.0
+        s.k[at + (0,)] = -1000.0
+    s.check(q, got)
+    # a weight of 0 does not keep NaN out, also where the key's part has no other weight
+    page, slot = int(s.table[0, 1]), 3
+    if type_ == "bf16":
+        s.cache.v[page, :, slot, 5] = math.nan
+    else:
+        s.cache.v.view(torch.uint8)[page, :, slot, 5] = 0x7F
+    out = s.attend(q)
+    assert out[:new, :, 5].isnan().all()
+    out[:new, :, 5] = got[:new, :, 5]
+    assert torch.equal(out, got)
