@@ -225,3 +225,34 @@ def test_non_finite_values_of_many_short_items(type_, hd):
     s.check(q, out)
     assert out.isfinite().any() and not out.isfinite().all()
     assert torch.equal(out.view(torch.int16), s.attend(q).view(torch.int16))
+
+
+@pytest.mark.parametrize("type_", ["bf16", "e4m3"])
+@pytest.mark.parametrize("starts", [
+    [0, 100, 4, 8, 12], [0, 3, 1, 9, 12], [-2, 3, 6, 9, 12], [0, 3, 6, 9, 13], [4, 8, 0, 4, 2],
+    [9, 3, 100, 5, 8] + [8] * 70 + [10, 0, 2, 1, 12]])
+def test_rows_are_written_and_read_wherever_the_attention_takes_them_from(type_, starts):
+    """Starts that decrease or leave the rows: those sequences have no rows, all others keep theirs."""
+    n = len(starts) - 1
+    s = Setup(type_, 2, 64, 16, [3] * n, [30] * n, seed=5)
+    s.row_start, s.n_rows, s.max_new = np.array(starts, np.int32), 12, 12
+    s.batch = s.make_batch()
+    k, v = (torch.from_numpy(s.rng.standard_normal((12, 2, 64)).astype(np.float32)).bfloat16().cuda() for _ in range(2))
+    B.armt_cache_write_bf16(k, v, s.cache, s.batch)
+    back = [torch.full((12, 2, 64), 7.0, dtype=torch.bfloat16, device="cuda") for _ in range(2)]
+    B.armt_cache_read_bf16(s.cache, s.batch, *back)
+    torch.cuda.synchronize()
+    placed = P.places(s.row_start, s.kv_len, s.table, 16, s.n_pages, 12, 12)
+    rows = [p[0] for p in placed]
+    assert set(rows)
+    for i, x in enumerate((k, v)):
+        want = x.double().cpu().numpy()
+        if type_ == "e4m3":
+            codes, sc = P.quantise(want)
+            want = P.e4m3_decode(codes) * np.exp2(sc.astype(np.float64) - 127)[..., None]
+        want[np.setdiff1d(np.arange(12), rows)] = 7.0
+        assert np.array_equal(back[i].double().cpu().numpy(), want)
+        pool = s.cache.k if i == 0 else s.cache.v
+        for row, b, pos, page in placed:
+            if type_ == "bf16" and rows.count(row) == 1 and page >= 0:
+                assert np.array_equal(pool[page, :, pos % 16].double().cpu().numpy(), want[row])
