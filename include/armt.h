@@ -405,12 +405,12 @@ typedef struct armt_kv_cache {
  *     not written, reads back as zeros and is not attended to;
  *   - n_b may be 0; a pair row_start[b], row_start[b + 1] that decreases or
  *     leaves [0, n_rows] counts as no rows (a row that starts in disorder give
- *     to two sequences gets either's output);
+ *     to two sequences is written and read for either, and gets either's output);
  *   - rows of a sequence past its first max_new, and rows that belong to no
  *     sequence, are left out: their outputs stay as they were.
  * Two sequences may share pages that only one or none of them writes. */
 typedef struct armt_paged_batch {
-  const int32_t* row_start;   /* device [n_seqs + 1], not decreasing */
+  const int32_t* row_start;   /* device [n_seqs + 1], not decreasing (the arrays 4-byte aligned) */
   const int32_t* kv_len;      /* device [n_seqs] */
   const int32_t* page_table;  /* device [n_seqs][table_width] */
   int64_t n_rows;             /* rows of the packed buffers, at most 2^31 - 1 */

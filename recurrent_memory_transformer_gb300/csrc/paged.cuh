@@ -122,6 +122,9 @@ inline armt_status check_cache(const armt_kv_cache* c) {
 inline armt_status check_batch(const armt_paged_batch* b, const armt_kv_cache* c) {
   if (b == nullptr || b->row_start == nullptr || b->kv_len == nullptr || b->page_table == nullptr)
     return refuse(ARMT_ERR_ARG, "NULL argument");
+  if ((reinterpret_cast<uintptr_t>(b->row_start) | reinterpret_cast<uintptr_t>(b->kv_len) |
+       reinterpret_cast<uintptr_t>(b->page_table)) & 3)
+    return refuse(ARMT_ERR_ARG, "row_start, kv_len and page_table must be 4-byte aligned");
   if (b->n_seqs <= 0 || b->table_width <= 0 || b->max_new <= 0 || b->n_rows < 0)
     return refuse(ARMT_ERR_ARG, "sizes must be positive");
   if (b->n_seqs > 65535) return refuse(ARMT_ERR_SHAPE, "n_seqs must be at most 65535");
