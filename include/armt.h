@@ -467,8 +467,9 @@ ARMT_API armt_status armt_paged_attention_bf16(const void* q, int64_t q_stride, 
                                                int64_t workspace_bytes, void* stream);
 
 /* Workspace of armt_paged_attention_bf16 on the current device, in bytes.  It
- * depends on the head layout, n_seqs, n_rows and max_new only (the batch's
- * arrays are not read) and does not grow with the cache. */
+ * depends on the device, the heads (n_q_heads, n_kv_heads, head_dim) and the
+ * smaller of n_rows and max_new only, not on the cache's type or size, and does
+ * not shrink as that grows: one for the largest batch serves all. */
 ARMT_API armt_status armt_paged_attention_workspace(const armt_kv_cache* cache, const armt_paged_batch* batch,
                                                     int32_t n_q_heads, int64_t* bytes);
 

@@ -546,8 +546,9 @@ def armt_paged_attention_workspace(cache, batch, n_q_heads) -> int:
 
 
 def paged_attention_workspace(cache, batch, n_q_heads):
-    """That workspace, allocated with torch.  One for all calls of a stream; calls that may
-    overlap on the device need one each."""
+    """That workspace, allocated with torch.  One for the batch with the most new rows a sequence
+    serves all calls with these heads on a stream, over either type of cache; calls that may overlap
+    on the device need one each."""
     import torch
     return torch.empty(armt_paged_attention_workspace(cache, batch, n_q_heads), dtype=torch.uint8,
                        device=cache.k.device)

@@ -6,6 +6,7 @@
 // (how, is said at the kernels).  Query heads of one kv head share its
 // keys, so a query tile's rows are (token, head of the group) pairs: row =
 // token * group + head.
+#include <algorithm>
 #include <type_traits>
 
 #include "paged_attn.cuh"
@@ -1387,6 +1388,27 @@ struct Shape {
   int64_t bytes;
 };
 
+template <int HD>
+int few_blocks(bool b16, int rows) {
+  return b16 ? few_blocks<HD, ARMT_CACHE_BF16>(rows) : few_blocks<HD, ARMT_CACHE_E4M3>(rows);
+}
+
+// Workspace for query tiles of up to `rows` rows of a kv head: the most that any
+// such call over either cache type needs, so that one sized for the largest batch
+// serves all others of the same heads.
+int64_t workspace_bytes(int hd, int group, int64_t rows, int sms) {
+  auto need = [&](int blocks, int tile) {
+    return (int64_t)blocks * (2 * tile * (hd + 4) * 4 + (int64_t)sizeof(PlanRange));
+  };
+  int64_t most = 0;
+  for (int tile = 8; tile <= (hd == 128 ? 32 : 64); tile *= 2) {
+    for (bool b16 : {false, true})
+      most = std::max(most, need((hd == 64 ? few_blocks<64>(b16, tile) : few_blocks<128>(b16, tile)) * sms, tile));
+    if (rows <= tile) return most;
+  }
+  return std::max(most, need(sms, tile_rows(group)));
+}
+
 Shape shape_of(const armt_kv_cache& c, const armt_paged_batch& b, int group, int sms) {
   Shape s;
   const int64_t rows = (b.max_new < b.n_rows ? (int64_t)b.max_new : b.n_rows) * group;
@@ -1397,12 +1419,9 @@ Shape shape_of(const armt_kv_cache& c, const armt_paged_batch& b, int group, int
   // its softmax is twice the work of its products, past 64 (83 for 60; 30 for 39).
   s.tiles = rows > (c.head_dim == 128 ? 32 : 64);
   s.rows = s.tiles ? tile_rows(group) : rows <= 8 ? 8 : rows <= 16 ? 16 : rows <= 32 ? 32 : 64;
-  int per_sm = 1;
-  if (!s.tiles)
-    per_sm = c.head_dim == 64 ? (b16 ? few_blocks<64, ARMT_CACHE_BF16>(s.rows) : few_blocks<64, ARMT_CACHE_E4M3>(s.rows))
-                              : (b16 ? few_blocks<128, ARMT_CACHE_BF16>(s.rows) : few_blocks<128, ARMT_CACHE_E4M3>(s.rows));
-  s.blocks = per_sm * sms;
-  s.bytes = (int64_t)s.blocks * (2 * s.rows * (c.head_dim + 4) * 4 + (int64_t)sizeof(PlanRange));
+  s.blocks = sms;
+  if (!s.tiles) s.blocks *= c.head_dim == 64 ? few_blocks<64>(b16, s.rows) : few_blocks<128>(b16, s.rows);
+  s.bytes = workspace_bytes(c.head_dim, group, rows, sms);
   return s;
 }
 

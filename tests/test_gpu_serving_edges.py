@@ -256,3 +256,28 @@ def test_rows_are_written_and_read_wherever_the_attention_takes_them_from(type_,
         for row, b, pos, page in placed:
             if type_ == "bf16" and rows.count(row) == 1 and page >= 0:
                 assert np.array_equal(pool[page, :, pos % 16].double().cpu().numpy(), want[row])
+
+
+@pytest.mark.parametrize("hd", [64, 128])
+@pytest.mark.parametrize("group", [1, 4, 5, 43, 64])
+def test_one_workspace_serves_smaller_batches_and_both_types(hd, group):
+    setups = {t: Setup(t, 1, hd, 16, [40], [90], seed=2) for t in ("bf16", "e4m3")}
+    sizes = {t: [B.armt_paged_attention_workspace(s.cache, s.make_batch(max_new=m), group)
+                 for m in (1, 2, 3, 4, 7, 8, 9, 16, 17, 32, 33, 40)] for t, s in setups.items()}
+    assert sizes["bf16"] == sizes["e4m3"] == sorted(sizes["bf16"])
+    # the number of sequences does not matter, fewer rows than max_new do
+    s = setups["bf16"]
+    two = B.PagedBatch(torch.zeros(3, dtype=torch.int32, device="cuda"), torch.zeros(2, dtype=torch.int32, device="cuda"),
+                       s.batch.page_table.repeat(2, 1), n_rows=40, max_new=40)
+    assert B.armt_paged_attention_workspace(s.cache, two, group) == sizes["bf16"][-1]
+    two = B.PagedBatch(two.row_start, two.kv_len, two.page_table, n_rows=3, max_new=40)
+    assert B.armt_paged_attention_workspace(s.cache, two, group) == sizes["bf16"][2]
+    workspace = torch.full((sizes["bf16"][-1],), 255, dtype=torch.uint8, device="cuda")
+    for t, s in setups.items():
+        for new in ([1], [3], [40]):
+            s.row_start = np.array([0] + new, np.int32)
+            s.max_new = new[0]
+            q = s.queries(group)
+            out = torch.full(q.shape, 7.0, dtype=torch.bfloat16, device="cuda")
+            B.armt_paged_attention_bf16(q, s.cache, s.make_batch(), out, workspace)
+            s.check(q, out)
