@@ -31,6 +31,7 @@
 
 #include "paged_attn.cuh"
 #include "paged_notes.h"
+#include "register_split.h"
 
 namespace armt {
 namespace {
@@ -49,7 +50,7 @@ struct TileCfg {
   static constexpr int THREADS = 32 * (CLEAN_WARP + CLEAN_WARPS);
   static constexpr int LAUNCH_REGS = B16 ? 168 : 128;
   static constexpr int SOFTMAX_REGS = 168, OTHER_REGS = 88;  // e4m3: 256 x 168 + 256 x 88 = 512 x 128
-  static_assert(B16 || kSoftmaxThreads * SOFTMAX_REGS + (THREADS - kSoftmaxThreads) * OTHER_REGS <= THREADS * LAUNCH_REGS,
+  static_assert(B16 || split_fits(LAUNCH_REGS, THREADS, kSoftmaxThreads, SOFTMAX_REGS, OTHER_REGS),
                 "the register split must fit what the block is launched with");
   static constexpr int ATOMS = HD / 64;       // 128-byte wide parts of a bf16 row
   static constexpr int BUF = kKeys * HD * 2;  // a tile of Q, K or V as bf16
@@ -721,8 +722,8 @@ armt_status launch(const PagedArgs& a, const PagedView& p, const armt_kv_cache& 
     cudaFuncAttributes at;
     if (e == cudaSuccess) e = cudaFuncGetAttributes(&at, tiles_kernel<HD, TYPE>);
     if (e != cudaSuccess) return launch_status(e, "paged attention set-up");
-    // fewer, and the softmax warps would wait for registers that nobody gives back
-    if (!C::B16 && at.numRegs != C::LAUNCH_REGS) return refuse(ARMT_ERR_CUDA, "paged attention: unexpected register count");
+    if (!C::B16 && !split_fits(at.numRegs, C::THREADS, kSoftmaxThreads, C::SOFTMAX_REGS, C::OTHER_REGS))
+      return refuse(ARMT_ERR_CUDA, "paged attention: unexpected register count");
     once.set(a.device);
   }
   const int slot_tokens = 128 / a.plan.group;
