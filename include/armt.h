@@ -483,8 +483,8 @@ ARMT_API armt_status armt_paged_attention_workspace(const armt_kv_cache* cache, 
  *                itself (with the same row distance), otherwise not overlapping
  * Columns at and past vocab are neither read nor written.  Logits of -inf have
  * probability 0; a row of only -inf gives zeros; with t > 0 a row with a NaN
- * or a +inf gives NaN.  fp32 throughout.  4-byte aligned pointers (16-byte aligned rows
- * are faster); n_rows 0 does nothing. */
+ * or a +inf gives NaN, and so does a t of NaN.  fp32 throughout.  4-byte aligned
+ * pointers (16-byte aligned rows are faster); n_rows 0 does nothing. */
 ARMT_API armt_status armt_token_probs(const float* logits, int64_t ld_logits, const float* temperature,
                                       int64_t n_rows, int32_t vocab, float* probs, int64_t ld_probs,
                                       void* stream);

@@ -95,7 +95,8 @@ __global__ void __launch_bounds__(kProbThreads) token_probs_kernel(const float* 
   float* dst = probs + row * ld_probs + first;
   const float t = temperature ? __ldg(temperature + row) : 1.f;
   const bool greedy = t <= 0.f;
-  const float c = fminf(1.4426950408889634f / t, 3.0e38f);  // a tiny t: 0 * c stays 0
+  float c = 1.4426950408889634f / t;
+  if (c > 3.0e38f) c = 3.0e38f;  // a tiny t: 0 * c stays 0 (and a NaN stays NaN)
   constexpr int HELD = RV > 0 ? RV : 1;
   float x[HELD][4];
   float m = -INFINITY;

@@ -281,3 +281,15 @@ def test_one_workspace_serves_smaller_batches_and_both_types(hd, group):
             out = torch.full(q.shape, 7.0, dtype=torch.bfloat16, device="cuda")
             B.armt_paged_attention_bf16(q, s.cache, s.make_batch(), out, workspace)
             s.check(q, out)
+
+
+@pytest.mark.parametrize("vocab", [37, 5000, 140001])
+def test_a_temperature_of_nan_gives_nan_and_the_other_rows_their_probabilities(vocab):
+    g = torch.Generator(device="cuda").manual_seed(3)
+    x = torch.randn(3, vocab, generator=g, device="cuda")
+    x[1, 5] = -math.inf
+    want, got = torch.empty_like(x), torch.empty_like(x)
+    B.armt_token_probs(x, want, torch.tensor([0.7, 1.0, 0.0], device="cuda"))
+    B.armt_token_probs(x, got, torch.tensor([0.7, math.nan, 0.0], device="cuda"))
+    assert got[1].isnan().all() and torch.equal(got[0], want[0]) and torch.equal(got[2], want[2])
+    assert not want.isnan().any()
