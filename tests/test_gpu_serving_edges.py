@@ -293,3 +293,75 @@ def test_a_temperature_of_nan_gives_nan_and_the_other_rows_their_probabilities(v
     B.armt_token_probs(x, got, torch.tensor([0.7, math.nan, 0.0], device="cuda"))
     assert got[1].isnan().all() and torch.equal(got[0], want[0]) and torch.equal(got[2], want[2])
     assert not want.isnan().any()
+
+
+# ------------------------------------------- paths that other tests leave out --
+
+@pytest.mark.parametrize("kv", [100, 9000])
+@pytest.mark.parametrize("hd,new", ROWS)
+def test_nan_codes_that_are_seen(hd, new, kv):
+    """NaN codes of an e4m3 cache, in values and keys of new rows: rows that see them get NaN, the others nothing of them."""
+    s = Setup("e4m3", 1, hd, 16, [new, 1], [kv, 40], seed=6)
+    codes = [x.view(torch.uint8).cpu().numpy() for x in (s.cache.k, s.cache.v)]
+
+    def put(pool, pos, col):
+        codes[pool][int(s.table[0, pos // 16]), 0, pos % 16, col] = 0x7F
+    put(1, kv - 1, 5)                                        # seen by the last row alone
+    put(1, kv - 1 - new // 2, 7)
+    put(1, kv - new, 9)                                      # by all of them
+    set_codes(s, k=codes[0], v=codes[1])
+    q = s.queries(4)
+    out = s.attend(q)
+    s.check(q, out)
+    assert out[new - 1, :, 5].isnan().all() and out[:new, :, 9].isnan().all() and out[new].isfinite().all()
+    put(0, kv - 1, 3)                                        # the last row all NaN
+    set_codes(s, k=codes[0])
+    out = s.attend(q)
+    s.check(q, out)
+    assert out[new - 1].isnan().all()
+    # and as the write makes them, of NaN and infinities
+    k, v = (torch.randn(s.n_rows, 1, hd, generator=torch.Generator().manual_seed(i)).bfloat16().cuda() for i in range(2))
+    v[0, 0, 1], v[new - 1, 0, 2], v[new - 1, 0, 3] = math.inf, -math.inf, math.nan
+    B.armt_cache_write_bf16(k, v, s.cache, s.batch)
+    set_codes(s)
+    out = s.attend(q)
+    s.check(q, out)
+    assert out[:new, :, 1].isnan().all() and out[new - 1, :, 2].isnan().all() and out[new].isfinite().all()
+
+
+@pytest.mark.parametrize("type_,hd,new", BOTH)
+def test_more_sequences_than_a_warp_has_lanes(type_, hd, new):
+    """The plan's sums over hundreds of sequences, each kernel; every third without rows, some with one."""
+    rng = np.random.default_rng(5)
+    kv = [int(x) for x in rng.integers(1, 120, 333)]
+    rows = [0 if b % 3 == 1 else 1 if b % 5 == 0 else min(new, k) for b, k in enumerate(kv)]
+    s = Setup(type_, 2, hd, 16, rows, kv, seed=8, max_new=new)
+    q = s.queries(4)
+    out = s.attend(q)
+    s.check(q, out)
+    assert torch.equal(out, s.attend(q))
+
+
+@pytest.mark.parametrize("type_,hd,new", BOTH)
+def test_hundreds_of_sequences_without_rows(type_, hd, new):
+    """A few active sequences among idle ones, in front, between and behind; and the same ones by themselves."""
+    n, active = 700, {0: 300, 350: 41, 351: 2000, 698: 77}
+    kv = [active.get(b, 50 if b % 2 else 0) for b in range(n)]
+    rows = [min(new, kv[b]) if b in active else 0 for b in range(n)]
+    s = Setup(type_, 1, hd, 16, rows, kv, seed=8, max_new=new)
+    q = s.queries(4)
+    out = s.attend(q)
+    s.check(q, out)
+    ids = sorted(active)
+    alone = B.PagedBatch(*(torch.from_numpy(np.ascontiguousarray(x)).cuda() for x in (
+        np.concatenate([[0], np.cumsum([rows[b] for b in ids])]).astype(np.int32), s.kv_len[ids], s.table[ids])),
+        n_rows=s.n_rows, max_new=new)
+    assert torch.equal(out, s.attend(q, batch=alone))
+
+
+@pytest.mark.parametrize("scale", [30.0, 1e-30, 1e4])
+@pytest.mark.parametrize("type_,hd,new", BOTH)
+def test_extreme_softmax_scales(type_, hd, new, scale):
+    s = Wide(type_, 1, hd, 32, [new, 1], [400, 90], seed=8)
+    q = s.queries(4)
+    s.check(q, s.attend(q, scale=scale), scale=scale)
