@@ -386,7 +386,8 @@ struct Model : ModelBase {
   // full-causal-attention LLaMA over a whole sequence (baseline): one
   // activation slot, grown on demand
   DevAllocs full_mem;
-  int64_t full_T = 0;
+  int64_t full_T = 0;  // tokens the workspace has room for
+  int64_t vt_T = 0;    // tokens of the call that Vtf is laid out for (0: none)
   // LM head: bf16 copy of a chunk of hidden rows (tensor-core path)
   DevAllocs lm_mem;
   AT* lm_rows = nullptr;
@@ -842,7 +843,7 @@ struct Model : ModelBase {
     if (T <= full_T) return ARMT_OK;
     CK(cudaStreamSynchronize(st));
     full_mem.free_all();
-    full_T = 0;
+    full_T = vt_T = 0;
     const armt_config& c = cfg;
     const size_t d = c.d_model, hd = c.head_dim, F = c.ffn_dim, Hq = c.n_q_heads, Hkv = c.n_kv_heads;
     const size_t tp = (size_t)((T + 7) / 8 * 8);
@@ -870,7 +871,6 @@ struct Model : ModelBase {
     bool ok = true;
     ok &= encode_tmap_bf16_3d(&tmNrmf, Nrmf, (int)d, (int)T, 1, TC_BM);
     ok &= encode_tmap_bf16_3d(&tmQKf, QKVf, (int)((Hq + Hkv) * hd), (int)T, 1, 128);
-    ok &= encode_tmap_bf16_3d(&tmVtf, Vtf, (int)tp, (int)hd, (int)Hkv, (int)hd);
     ok &= encode_tmap_bf16_3d(&tmAttf, Attf, (int)(Hq * hd), (int)T, 1, TC_BM);
     ok &= encode_tmap_bf16_3d(&tmUf, Uf, (int)F, (int)T, 1, TC_BM);
     if (!ok) return fail(ARMT_ERR_CUDA, "cuTensorMapEncodeTiled failed");
@@ -954,6 +954,15 @@ struct Model : ModelBase {
       const int Hq = c.n_q_heads, Hkv = c.n_kv_heads, Nq = n_qkv();
       const int tp = (T + 7) / 8 * 8;
       const long long Td = (long long)T * d;
+      // the rows of V^T are as far apart as this call's tokens make them; the
+      // columns that pad them to a multiple of 8 are zeros
+      if (vt_T != T) {
+        vt_T = 0;
+        if (!encode_tmap_bf16_3d(&tmVtf, Vtf, tp, hd, Hkv, hd))
+          return fail(ARMT_ERR_CUDA, "cuTensorMapEncodeTiled failed");
+        CK(cudaMemsetAsync(Vtf, 0, (size_t)Hkv * hd * tp * sizeof(QT), st));
+        vt_T = T;
+      }
       CKS(prof_begin(ARMT_KC_OTHER, st));
       embed_gather_kernel<WT><<<dim3(T, 1), 256, 0, st>>>(tokens, 0, embed, memtok, Xf, (WT*)nullptr, T, T, 0,
                                                          d, c.vocab);
