@@ -365,3 +365,93 @@ def test_extreme_softmax_scales(type_, hd, new, scale):
     s = Wide(type_, 1, hd, 32, [new, 1], [400, 90], seed=8)
     q = s.queries(4)
     s.check(q, s.attend(q, scale=scale), scale=scale)
+
+
+# -------------------------------------------------------- with the model --
+
+def test_a_continued_sequence_equals_the_whole_one_through_the_model():
+    """The full-attention baseline's layers around the cache and the attention, fed a prompt's chunk, then drafted tokens,
+    then single ones, for two packed sequences: the hidden states of armt_forward_full_attention over the whole sequences.
+
+    Weight products are the library's; norms, rotary embedding and SwiGLU are written out here.  Against the definition in
+    64 bits the error stays within 1.5 times that of ideal arithmetic with the same operands rounded to bf16, the factor
+    that tests/test_gpu_parity.py measures; so do the baseline's own (with fp16 operands in its attention), and the two
+    therefore differ by no more than the sum."""
+    import dataclasses
+
+    from oracle import armt_oracle as O
+    from recurrent_memory_transformer_gb300 import inputs as I
+    cfg = dataclasses.replace(I.ARMT_1B, n_layers=2, vocab=4096)
+    W = I.make_weights(cfg, seed=61, norm_jitter=0.1)
+    m = B.Model(cfg, B.device_weight_tensors(cfg, W))
+    lens = [230, 130]
+    tok = [np.random.default_rng(61 + b).integers(0, cfg.vocab, size=n).astype(np.int32) for b, n in enumerate(lens)]
+    hq, hkv, hd, d = cfg.n_q_heads, cfg.n_kv_heads, cfg.head_dim, cfg.d_model
+    wide = {k: torch.from_numpy(np.asarray(v, np.float32)).cuda() for k, v in W.items()}
+
+    def norm(x, gain):
+        x = x.double()
+        return (x / (x.square().mean(-1, keepdim=True) + cfg.norm_eps).sqrt() * gain.double()).bfloat16()
+
+    def product(x, w):
+        out = torch.empty(1, x.shape[0], w.shape[0], dtype=torch.float32, device="cuda")
+        B.armt_grouped_gemm_bf16(x.contiguous()[None], w.bfloat16().contiguous()[None], out)
+        return out[0]
+
+    def rope(x, pos):
+        half = hd // 2
+        angle = pos.double()[:, None, None] * (cfg.rope_base ** (-2.0 * torch.arange(half, device="cuda").double() / hd))
+        a, b = x.double()[..., :half], x.double()[..., half:]
+        return torch.cat([a * angle.cos() - b * angle.sin(), b * angle.cos() + a * angle.sin()], -1).bfloat16()
+
+    pages = torch.randperm(40, generator=torch.Generator().manual_seed(1)).int().cuda()[:36].view(2, 18)[:, :15].contiguous()
+    caches = [B.KvCache.allocate(40, 16, hkv, hd) for _ in range(cfg.n_layers)]
+    got = [torch.empty(n, d, device="cuda") for n in lens]
+    done = [0, 0]
+    steps = [(180, 100), (5, 3), (1, 5), (4, 0)] + [(1, 1)] * 40
+    for step in steps:
+        new = [min(n, total - at) for n, total, at in zip(step, lens, done)]
+        if not sum(new):
+            continue
+        done = [at + n for at, n in zip(done, new)]
+        batch = B.PagedBatch(torch.tensor([0, new[0], sum(new)], dtype=torch.int32, device="cuda"),
+                             torch.tensor(done, dtype=torch.int32, device="cuda"), pages, sum(new), max(new))
+        workspace = B.paged_attention_workspace(caches[0], batch, hq)
+        pos = torch.cat([torch.arange(at - n, at, device="cuda") for n, at in zip(new, done)])
+        ids = torch.from_numpy(np.concatenate([t[at - n:at] for t, n, at in zip(tok, new, done)])).long().cuda()
+        x = wide["embed"][ids]
+        for l, cache in enumerate(caches):
+            n1 = norm(x, wide["norm1"][l])
+            q, k, v = (product(n1, wide[w][l]).unflatten(1, (-1, hd)) for w in ("wq", "wk", "wv"))
+            B.armt_cache_write_bf16(rope(k, pos), v.bfloat16(), cache, batch)
+            out = torch.empty(sum(new), hq, hd, dtype=torch.bfloat16, device="cuda")
+            B.armt_paged_attention_bf16(rope(q, pos), cache, batch, out, workspace)
+            x = x + product(out.flatten(1), wide["wo"][l])
+            n2 = norm(x, wide["norm2"][l])
+            gate, up = product(n2, wide["w_gate"][l]), product(n2, wide["w_up"][l])
+            x = x + product((torch.nn.functional.silu(gate.double()) * up.double()).bfloat16(), wide["w_down"][l])
+        y = x.double()
+        y = y / (y.square().mean(-1, keepdim=True) + cfg.norm_eps).sqrt() * wide["norm_f"].double()
+        for b, part in enumerate(y.float().split(new)):
+            got[b][done[b] - new[b]:done[b]] = part
+    assert done[0] >= 229 and done[1] == lens[1]
+    B.armt_block_sync_status()
+
+    def plain(rounding, t):
+        W64 = O.widen_weights(W)
+        x = W64["embed"][t]
+        for l in range(cfg.n_layers):
+            x = O.llama_block(x, cfg, W64, l, rounding)
+        return O.rmsnorm(x, W64["norm_f"], cfg.norm_eps)
+    for b, n in enumerate(done):
+        h = torch.empty((n, d), dtype=torch.float32, device="cuda")
+        m.armt_forward_full_attention(torch.from_numpy(tok[b][:n]).cuda(), h)
+        m.armt_sync_status()
+        exact = plain(O.EXACT, tok[b][:n])
+        ideal = np.abs(plain(O.OperandRounding(O.round_bf16, O.round_bf16), tok[b][:n]) - exact).max()
+        half = np.abs(plain(O.ROUNDING["bf16"], tok[b][:n]) - exact).max()
+        here = got[b][:n].double().cpu().numpy()
+        assert np.abs(here - exact).max() <= 1.5 * ideal, (np.abs(here - exact).max(), ideal)
+        assert np.abs(here - h.double().cpu().numpy()).max() <= 1.5 * (ideal + half)
+        assert (here * exact).sum() / np.linalg.norm(here) / np.linalg.norm(exact) >= 0.999
+    m.close()
