@@ -156,14 +156,13 @@ __device__ __forceinline__ float scale_exponent(uint32_t byte) {
 }
 
 // What a row's sum of products in reference m is multiplied by, one after the
-// other, for its output: 1 / l, l in reference u (without weights: `empty`), and
+// other, for its output: 1 / l, l in reference u (see weight_share), and
 // 2^(m - u) in two halves (it may be 2^140).
 struct RowFactors {
   float first, second;
 };
-template <typename Empty>
-__device__ __forceinline__ RowFactors row_factors(float l, float m, float u, Empty empty) {
-  const float inv = l == 0.f ? empty() : 1.f / l;
+__device__ __forceinline__ RowFactors row_factors(float l, float m, float u) {
+  const float inv = weight_share(l, m);
   const float half = m == u ? 1.f : fast_exp2(0.5f * (m - u));
   return RowFactors{inv * half, half};
 }
@@ -313,6 +312,7 @@ __global__ void __launch_bounds__(kThreads + 32, RowsCfg<HD, TYPE, 0, WM>::BLOCK
   int seen_min = 0, seen_max = 0;
   bool noted = false;  // this thread has written to `bad` for the query tile
   bool wide = false;   // this warp's sums have two references (the same for all its lanes)
+  int paged_from = 0;  // the first key of the item, in this block's part of it, that has a page
 
   // reads the rows of the query tile at `at`, and starts its sums
   auto start_item = [&]() {
@@ -608,6 +608,7 @@ __global__ void __launch_bounds__(kThreads + 32, RowsCfg<HD, TYPE, 0, WM>::BLOCK
     [[maybe_unused]] float u[2];  // codes: the reference of l
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
+      m[h] = seen_reference(m[h], paged_from < visible[h]);
       if constexpr (!B16) u[h] = wide ? sum_ref[warp][r + 8 * h] : m[h];
       l[h] += __shfl_xor_sync(0xffffffffu, l[h], 1);
       l[h] += __shfl_xor_sync(0xffffffffu, l[h], 2);
@@ -680,12 +681,12 @@ __global__ void __launch_bounds__(kThreads + 32, RowsCfg<HD, TYPE, 0, WM>::BLOCK
           const int tok = row / a.plan.group, head = at.head * a.plan.group + row % a.plan.group;
           bf16* dst = a.out + (long long)(at.row0 + tok) * a.out_stride + head * HD;
           if constexpr (B16) {
-            const float inv = l[h] == 0.f ? empty_row(p, at.b, visible[h]) : 1.f / l[h];
+            const float inv = weight_share(l[h], m[h]);
 #pragma unroll
             for (int t = 0; t < NT; ++t)
               *reinterpret_cast<uint32_t*>(dst + 8 * t + 2 * c) = pack_bf16x2(o[t][2 * h] * inv, o[t][2 * h + 1] * inv);
           } else {
-            const RowFactors f = row_factors(l[h], m[h], u[h], [&] { return empty_row(p, at.b, visible[h]); });
+            const RowFactors f = row_factors(l[h], m[h], u[h]);
             auto two = [&](float x, float y) {
               return pack_bf16x2(x * f.first * f.second, y * f.first * f.second);
             };
@@ -730,6 +731,7 @@ __global__ void __launch_bounds__(kThreads + 32, RowsCfg<HD, TYPE, 0, WM>::BLOCK
   for (bool more = true; more; more = plan_next_item(a.plan, p, range, at)) {
     const int count = plan_here(range, at);
     start_item();
+    paged_from = 0x7fffffff;
     for (int j = 0; j < count; ++j) {
       // a warp whose wait gives up keeps to the loop, and with it to the barriers
       // that the four warps share: later waits give up at once
@@ -737,7 +739,9 @@ __global__ void __launch_bounds__(kThreads + 32, RowsCfg<HD, TYPE, 0, WM>::BLOCK
           0xffffffffu, mbar_wait_bounded(&sh.full[stage], phase, err, DEV_TIMEOUT_FULL, a.wp.limit_ns));
       const int k0 = (at.tile + j) * kKeys;
       if (got && k0 < seen_max) {  // some row sees the tile
-        const bool all = k0 + kKeys <= seen_min && sh.with_page[stage] == 15u;
+        const uint32_t have = sh.with_page[stage];
+        const bool all = k0 + kKeys <= seen_min && have == 15u;
+        if (have != 0) paged_from = min(paged_from, k0 + 16 * (__ffs((int)have) - 1));
         const std::false_type no;
         const std::true_type yes;
         if constexpr (B16) {
@@ -807,6 +811,7 @@ __global__ void __launch_bounds__(kThreads + 32, RowsCfg<HD, TYPE, NB>::BLOCKS)
   float m[NB][2], l[NB][2];
   int seen_min = 0, seen_max = 0;
   bool noted = false, wide = false;
+  int paged_from = 0;
 
   auto start_item = [&]() {
     const int rows = at.n * a.plan.group;
@@ -1071,6 +1076,7 @@ __global__ void __launch_bounds__(kThreads + 32, RowsCfg<HD, TYPE, NB>::BLOCKS)
       for (int j = 0; j < 2; ++j) {
 #pragma unroll
         for (int d = 4; d < 32; d <<= 1) l[nb][j] += __shfl_xor_sync(0xffffffffu, l[nb][j], d);
+        m[nb][j] = seen_reference(m[nb][j], paged_from < visible_to_row[8 * nb + 2 * c + j]);
         if (r == 0) {
           const int row = 8 * nb + 2 * c + j;
           stats[warp * R + row] = make_float2(m[nb][j], l[nb][j]);
@@ -1125,8 +1131,7 @@ __global__ void __launch_bounds__(kThreads + 32, RowsCfg<HD, TYPE, NB>::BLOCKS)
       RowFactors f[2];
 #pragma unroll
       for (int j = 0; j < 2; ++j)
-        f[j] = row_factors(l[nb][j], m[nb][j], B16 ? m[nb][j] : u[nb][j],
-                           [&] { return whole ? empty_row(p, at.b, visible_to_row[8 * nb + 2 * c + j]) : 0.f; });
+        f[j] = row_factors(l[nb][j], m[nb][j], B16 ? m[nb][j] : u[nb][j]);
 #pragma unroll
       for (int t0 = 0; t0 < KS; t0 += 4) {
         consumers_sync();  // the statistics, or the tiles before, have been read
@@ -1196,12 +1201,15 @@ __global__ void __launch_bounds__(kThreads + 32, RowsCfg<HD, TYPE, NB>::BLOCKS)
   for (bool more = true; more; more = plan_next_item(a.plan, p, range, at)) {
     const int count = plan_here(range, at);
     start_item();
+    paged_from = 0x7fffffff;
     for (int j = 0; j < count; ++j) {
       const bool got = __all_sync(
           0xffffffffu, mbar_wait_bounded(&sh.full[stage], phase, err, DEV_TIMEOUT_FULL, a.wp.limit_ns));
       const int k0 = (at.tile + j) * kKeys;
       if (got && k0 < seen_max) {  // some row sees the tile
-        const bool all = k0 + kKeys <= seen_min && sh.with_page[stage] == 15u;
+        const uint32_t have = sh.with_page[stage];
+        const bool all = k0 + kKeys <= seen_min && have == 15u;
+        if (have != 0) paged_from = min(paged_from, k0 + 16 * (__ffs((int)have) - 1));
         const std::false_type no;
         const std::true_type yes;
         if constexpr (B16) {
@@ -1323,8 +1331,7 @@ __global__ void __launch_bounds__(256, TWO ? 3 : 4) join_kernel(const PagedArgs 
       }
       const int row = at.qt * R + base + grp;
       const int tok = row / a.plan.group, head = at.head * a.plan.group + row % a.plan.group;
-      const RowFactors f =
-          row_factors(sum, m, TWO ? up : m, [&] { return empty_row(p, at.b, plan_visible(at, tok)); });
+      const RowFactors f = row_factors(sum, m, TWO ? up : m);
 #pragma unroll
       for (int i = 0; i < 4; ++i) o[i] *= f.first;
       if constexpr (TWO) {

@@ -48,15 +48,17 @@ __device__ __forceinline__ float poison_of(const Poison& t, int visible) {
   return v;
 }
 
-// What stands for 1 / (sum of weights) in a row whose weights are all zero: 0 if
-// none of the keys it could see has a page, so that it attends to nothing; NaN if
-// one has, whose scores are then all -inf: softmax is 0 / 0 there.  (Rare, and
-// over at the first page that is there.)
-__device__ __forceinline__ float empty_row(const PagedView& p, int b, int visible) {
-#pragma unroll 1
-  for (long long pos = 0; pos < visible; pos += 1ll << p.page_shift)
-    if (paged_page(p, b, pos) >= 0) return NAN;
-  return 0.f;
+// Rows without weights.  One that attends to nothing gives zeros; one that
+// attends to keys whose scores are all -inf is 0 / 0 in the softmax and gives NaN.
+// The second kind leaves the loops with the reference -inf like the first, and
+// takes the lowest number for it instead, which says so to the joining kernel too
+// and weighs nothing beside any part with weights.
+__device__ __forceinline__ float seen_reference(float m, bool sees_a_key) {
+  return m == -INFINITY && sees_a_key ? -3.402823466e38f : m;
+}
+// 1 / (sum of weights), or what stands for it in such rows.
+__device__ __forceinline__ float weight_share(float l, float m) {
+  return l != 0.f ? 1.f / l : m == -INFINITY ? 0.f : NAN;
 }
 
 // Tensor map of a pool: rows of head_dim elements, page_size of them, a page

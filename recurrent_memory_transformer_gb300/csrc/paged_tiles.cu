@@ -83,6 +83,7 @@ struct TileBars {
   int any_bad;
   PlanRange range;
   uint32_t with_page[16];  // of tile t at t % 16: 8 bits, which 16-key groups have a page
+  int paged_from[4];       // of item i at i % 4: the first key, in this block's part, that has a page
 };
 
 // D[tmem] (+)= A[tmem] * B[smem], kind::f16.
@@ -209,7 +210,7 @@ __global__ void __launch_bounds__(TileCfg<HD, TYPE>::THREADS, 1)
     struct {
       int ids, at, b;
     } look[2] = {{-1, 0, -1}, {-1, 0, -1}};  // page ids of 32 runs, for K and for V (which trails)
-    int n = 0, items = 0, tiles = 0;
+    int n = 0, items = 0, tiles = 0, paged_from = 0;
     bool ok = true;
     // the copies of tile `tile` of K (pool 0) or V (1) into the next buffer
     auto load = [&](int pool, int tile, int count) {
@@ -233,6 +234,8 @@ __global__ void __launch_bounds__(TileCfg<HD, TYPE>::THREADS, 1)
           uint32_t groups = 0;
           for (int j = 0; j < runs; ++j) groups |= (have >> j & 1u) * (run_bits << (j * run / 16));
           bar.with_page[count % 16] = groups;
+          if (groups != 0) paged_from = min(paged_from, k0 + 16 * (__ffs((int)groups) - 1));
+          bar.paged_from[(items - 1) % 4] = paged_from;
         }
         mbar_arrive_expect_tx(&full[b], (uint32_t)(__popc(have) * run * (B16 ? HD * 2 : HD + 1)));
       }
@@ -271,6 +274,7 @@ __global__ void __launch_bounds__(TileCfg<HD, TYPE>::THREADS, 1)
       items = __shfl_sync(0xffffffffu, items, 0);
       ok = __shfl_sync(0xffffffffu, (int)ok, 0);
       if (!ok) break;
+      paged_from = 0x7fffffff;
       load(0, at.tile, tiles);
       for (int j = 0; ok && j < count; ++j) {
         load(1, at.tile + j, tiles + j);
@@ -648,7 +652,8 @@ __global__ void __launch_bounds__(TileCfg<HD, TYPE>::THREADS, 1)
       if (got && ok) {
         tc_fence_after();
         const bool poisoned = bar.any_bad != 0;
-        const float inv = l != 0.f ? 1.f / l : whole ? empty_row(p, at.b, visible) : 0.f;
+        m = seen_reference(m, bar.paged_from[items % 4] < visible);
+        const float inv = weight_share(l, m);
         bf16* dst = a.out + (long long)(at.row0 + tok) * a.out_stride +
                     (at.head * a.plan.group + r % a.plan.group) * HD;
 #pragma unroll 1

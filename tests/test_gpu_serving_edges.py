@@ -455,3 +455,19 @@ def test_a_continued_sequence_equals_the_whole_one_through_the_model():
         assert np.abs(here - h.double().cpu().numpy()).max() <= 1.5 * (ideal + half)
         assert (here * exact).sum() / np.linalg.norm(here) / np.linalg.norm(exact) >= 0.999
     m.close()
+
+
+@pytest.mark.parametrize("type_,hd,new", BOTH)
+def test_long_contexts_without_pages(type_, hd, new):
+    """Tables of 65,536 pages that are all missing give zeros, beside a sequence whose only page, thousands of missing ones
+    in, has scores of -inf: NaN."""
+    s = Setup(type_, 1, hd, 16, [new] * 3, [40] * 3, seed=4, width=65536)
+    table = torch.full((3, 65536), -1, dtype=torch.int32, device="cuda")
+    table[1, 60000] = int(s.table[0, 0])
+    s.table[1, 0] = s.table[0, 0]
+    minus_infinity(s, 1, range(16))
+    lens = torch.full((3,), 65536 * 16, dtype=torch.int32, device="cuda")
+    q = first_column(s)
+    out = s.attend(q, batch=B.PagedBatch(s.batch.row_start, lens, table, s.n_rows, new))
+    B.armt_block_sync_status()
+    assert (out[:new] == 0).all() and out[new:2 * new].isnan().all() and (out[2 * new:] == 0).all()
