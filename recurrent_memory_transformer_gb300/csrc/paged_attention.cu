@@ -38,8 +38,14 @@ namespace {
 // Work is dealt out in tiles, not in sequences: every block takes an equal,
 // contiguous range of the list of (sequence, kv head, query tile, key tile),
 // so ragged batches balance by construction; a sequence whose tiles fall to
-// several blocks leaves partial sums (fp32, with their maximum) that the
-// joining kernel adds in block order.
+// several blocks leaves parts (fp32 sums with their references) that the joining
+// kernel adds in block order.
+//
+// What is held in fewer than 32 bits: the weights, as operands of the second
+// product, which takes 16-bit ones: rounded to V's bf16 (2^-8 of each), over codes
+// to fp16 (2^-11).  Their sum is taken in fp32 before that.  Against 64 bits the
+// outputs are off by 0.0021 to 0.0023 (bf16) and 0.0017 (codes) of their size, of
+// which the rounding of the output to bf16 alone is 0.0017.
 //
 // e4m3 caches: codes go to fp16 by one conversion instruction for two values
 // (exact), the products run on fp16 with q scaled by a power of two per row
@@ -83,7 +89,7 @@ struct RowsCfg {
   static constexpr int QUERIES = NB * HD * 16;  // turned: the queries' fragments
   // as many buffers, up to 6, as those blocks find room for beside a KB that
   // each block costs, its static shared memory and a KB of alignment
-  static constexpr int ROOM = 233472 / BLOCKS - 1024 - (12 * HD + 768) - 1024 - JOIN - QUERIES;
+  static constexpr int ROOM = 233472 / BLOCKS - 1024 - (12 * HD + 1024) - 1024 - JOIN - QUERIES;
   static constexpr int STAGES = ROOM / STAGE < 6 ? ROOM / STAGE : 6;
   static_assert(STAGES >= 2, "a buffer to fill beside the one in use");
   static constexpr int SMEM = 1024 + STAGES * STAGE + JOIN + QUERIES;
@@ -1420,10 +1426,15 @@ Shape shape_of(const armt_kv_cache& c, const armt_paged_batch& b, int group, int
   Shape s;
   const int64_t rows = (b.max_new < b.n_rows ? (int64_t)b.max_new : b.n_rows) * group;
   const bool b16 = c.type == ARMT_CACHE_BF16;
-  // Past 32 rows of head_dim 128 the tensor-core kernel is the faster one (16
-  // sequences of 10 or 14 tokens, 32 / 8 heads, contexts to 8K: 98 for 113 us,
-  // e4m3 134 for 125; 2 sequences 38 for 50, 45 for 61), with head_dim 64, where
-  // its softmax is twice the work of its products, past 64 (83 for 60; 30 for 39).
+  // Past 32 rows of head_dim 128 the tensor-core kernel is the faster one over
+  // either type.  bf16, 16 sequences of 10 or 14 tokens, 32 / 8 heads, contexts to
+  // 8K: 98 us for 113; 2 sequences 38 for 50.  e4m3, 9 / 12 / 16 tokens: 16
+  // sequences 131 / 133 / 132 for 147 / 155 / 162, 2 sequences 55 / 56 / 56 for 79 /
+  // 84 / 87, 64 sequences 425 / 425 / 427 for 457 / 471 / 496 (the few-row kernel's
+  // sums spill there); only many long contexts go the other way (16 of 30,000
+  // tokens: 638 for 550).  The weights are then bf16 for fp16.  With head_dim 64,
+  // where its softmax is twice the work of its products, past 64 rows (83 for 60;
+  // 30 for 39).
   s.tiles = rows > (c.head_dim == 128 ? 32 : 64);
   s.rows = s.tiles ? tile_rows(group) : rows <= 8 ? 8 : rows <= 16 ? 16 : rows <= 32 ? 32 : 64;
   s.blocks = sms;

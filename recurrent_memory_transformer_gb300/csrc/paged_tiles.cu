@@ -23,8 +23,13 @@
 // tensor core runs its products in the order they were issued: once S_s(j+1)
 // has arrived, PV_s(j) has ended, and O_s may be touched until P_s(j+1) is
 // handed over.  A row's reference maximum moves only when a tile's maximum
-// passes it by more than 2^8 (the weights then stay below 2^8, exact enough
-// in bf16 at any scale), which makes rescaling O rare.
+// passes it by more than 2^8, which makes rescaling O rare.
+//
+// What is held in fewer than 32 bits: the weights, rounded to bf16 (2^-8 of each,
+// at any scale) because both operands of a product have one type and V is bf16;
+// their sum is taken in fp32 before that, the references and O are fp32.  Against
+// 64 bits the outputs are off by 0.0023 of their size, 0.0017 of it their own
+// rounding to bf16.
 //
 // Blocks take equal shares of the list of tiles; see paged_plan.cuh.
 #include <type_traits>
@@ -43,8 +48,8 @@ template <int HD, int TYPE>
 struct TileCfg {
   static constexpr bool B16 = TYPE == ARMT_CACHE_BF16;
   // Cleaning alone is little work for two warps; expanding takes six (2 x
-  // 1,024 rows over 16K: 631 us, 685 with four), and then the softmax warps
-  // need registers that the others give back.  (With four and the exchange
+  // 1,024 rows over 16K, 680 us now: 631 for 685 with four when both were there),
+  // and then the softmax warps need registers that the others give back.  (With four and the exchange
   // the bf16 kernel was a tenth slower, 533 us for 479.)
   static constexpr int CLEAN_WARP = 10, CLEAN_WARPS = B16 ? 2 : 6;
   static constexpr int THREADS = 32 * (CLEAN_WARP + CLEAN_WARPS);
