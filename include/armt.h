@@ -472,7 +472,7 @@ ARMT_API armt_status armt_cache_read_bf16(const armt_kv_cache* cache, const armt
  * The whole call runs on one kernel, chosen by max_new (and the heads): 63 single
  * tokens beside a chunk of 512 take 300 to 500 us in one call and 205 to 310 in
  * two, so give chunks a call of their own.  A sequence without rows costs about
- * 0.4 us when it comes after the last one with rows, less before (8 sequences in
+ * 0.35 us when it comes after the last one with rows, less before (8 sequences in
  * front of 504 idle ones 220 us, spread among them 74, alone 47). */
 ARMT_API armt_status armt_paged_attention_bf16(const void* q, int64_t q_stride, const armt_kv_cache* cache,
                                                const armt_paged_batch* batch, int32_t n_q_heads, float scale,
