@@ -300,10 +300,11 @@ ARMT_API armt_status armt_segment_attention_bf16(const void* qk, const void* vt,
 /* Status of the two building blocks above and of armt_paged_attention_bf16,
  * which run without a model: waits for `stream`, then reports
  * ARMT_ERR_TIMEOUT if a bounded device-side wait of any of them gave up on the
- * current device since the last call, and clears it.  Their error words are
- * device globals of the library (one set per device); a word stays set until
- * read, and while it is set its blocks' waits give up early, so their outputs
- * are then undefined.  Allocates nothing. */
+ * current device since the last call, and clears it.  Their error word is a
+ * device global of the library (one per device, looked up on the first call
+ * with the device current); it stays set until read, and while it is set the
+ * blocks' waits give up early, so their outputs are then undefined.  Allocates
+ * nothing. */
 ARMT_API armt_status armt_block_sync_status(void* stream);
 
 /* Fixed device scratch of armt_segment_attention_bf16_noalloc (bytes). */

@@ -118,7 +118,6 @@ bool encode_tmap_tiled3(CUtensorMap* map, const void* base, CUtensorMapDataType 
   return fn(map, type, 3, const_cast<void*>(base), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, swizzle,
             CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
-cudaError_t take_paged_error(int* code);
 }  // namespace armt
 
 // ------------------------------------------------------- allocation --
@@ -1567,8 +1566,7 @@ static armt_status block_err_word(int dev, int** out) {
   int* p = w.ptr.load();
   if (p == nullptr || w.ctx.load() != ctx) {
     void* a = nullptr;
-    CK(cudaGetSymbolAddress(&a, g_block_err));
-    CK(cudaMemset(a, 0, sizeof(int)));
+    CK(cudaGetSymbolAddress(&a, g_block_err));  // (zero in a fresh context; no device work, which a capture would refuse)
     w.ptr.store(static_cast<int*>(a));
     w.ctx.store(ctx);
     p = static_cast<int*>(a);
@@ -1631,6 +1629,7 @@ armt_status ready_device(int* dev, int* num_sms) {
   if (*dev >= 0 && *dev < 64) sms_of[*dev].store(*num_sms);
   return ARMT_OK;
 }
+armt_status block_error_word(int dev, int** word) { return block_err_word(dev, word); }
 }  // namespace armt
 
 extern "C" {
@@ -1917,11 +1916,9 @@ armt_status armt_block_sync_status(void* stream) {
   CKS(check_device(&dev));
   CKS(block_err_word(dev, &err));
   CK(cudaStreamSynchronize(reinterpret_cast<cudaStream_t>(stream)));
-  int h = 0, paged = 0;
+  int h = 0;
   CK(cudaMemcpy(&h, err, sizeof(int), cudaMemcpyDeviceToHost));
   if (h != 0) CK(cudaMemset(err, 0, sizeof(int)));
-  CK(take_paged_error(&paged));
-  if (h == 0) h = paged;
   if (h != 0) return fail(ARMT_ERR_TIMEOUT, "device wait timed out (code " + std::to_string(h) + ")");
   return ARMT_OK;
 }

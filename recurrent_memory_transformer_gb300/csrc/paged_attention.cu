@@ -95,9 +95,6 @@ struct RowsCfg {
   static constexpr int SMEM = 1024 + STAGES * STAGE + JOIN + QUERIES;
 };
 
-// Set by a bounded wait that gave up; read and cleared by armt_block_sync_status.
-__device__ int g_paged_err;
-
 // Barrier of the consumer warps.
 __device__ __forceinline__ void consumers_sync() { asm volatile("bar.sync 1, 128;" ::: "memory"); }
 
@@ -207,7 +204,7 @@ __device__ __forceinline__ void produce(const CUtensorMap& tm_k, const CUtensorM
                                         const PagedView& p, const PlanRange& range, RowsShared<C>& sh, uint8_t* smem) {
   constexpr bool B16 = C::B16;
   const int lane = threadIdx.x & 31;
-  int* err = &g_paged_err;
+  int* err = a.err;
   PlanCursor at = range.first;
   const int run = min(1 << p.page_shift, kKeys);  // keys of a tile that share a page
   const uint32_t run_bits = (1u << (run / 16)) - 1u;
@@ -292,7 +289,7 @@ __global__ void __launch_bounds__(kThreads + 32, RowsCfg<HD, TYPE, 0, WM>::BLOCK
   const int r = lane >> 2, c = lane & 3;
   const uint32_t sbase = smem_u32(smem);
   float* join = reinterpret_cast<float*>(smem + C::STAGES * C::STAGE);
-  int* err = &g_paged_err;
+  int* err = a.err;
 
   for (int i = tid; i < HD; i += kThreads + 32) bad[i] = Poison{0x7fffffff, 0x7fffffff, 0x7fffffff};
   init_barriers<C>(sh);
@@ -798,7 +795,7 @@ __global__ void __launch_bounds__(kThreads + 32, RowsCfg<HD, TYPE, NB>::BLOCKS)
   const uint32_t sbase = smem_u32(smem);
   float* join = reinterpret_cast<float*>(smem + C::STAGES * C::STAGE);
   uint2* queries = reinterpret_cast<uint2*>(smem + C::STAGES * C::STAGE + C::JOIN);  // [NB][KS][lane]
-  int* err = &g_paged_err;
+  int* err = a.err;
 
   for (int i = tid; i < HD; i += kThreads + 32) bad[i] = Poison{0x7fffffff, 0x7fffffff, 0x7fffffff};
   init_barriers<C>(sh);
@@ -1473,18 +1470,6 @@ cudaError_t launch_join(const PagedArgs& a, const PagedView& p, int head_dim, bo
   return cudaLaunchKernelEx(&cfg, head_dim == 64 ? join_kernel<64, false> : join_kernel<128, false>, a, p);
 }
 
-// Waits that gave up in the attention's kernels on the current device since the
-// last look (0: none), after `stream` has been waited for.
-cudaError_t take_paged_error(int* code) {
-  cudaError_t e = cudaMemcpyFromSymbol(code, g_paged_err, sizeof(int));
-  const int zero = 0;
-  if (e == cudaSuccess && *code != 0) e = cudaMemcpyToSymbol(g_paged_err, &zero, sizeof(int));
-  int tiles = 0;
-  if (e == cudaSuccess) e = take_tiles_error(&tiles);
-  if (*code == 0) *code = tiles;
-  return e;
-}
-
 }  // namespace armt
 
 using namespace armt;
@@ -1538,6 +1523,7 @@ extern "C" ARMT_API armt_status armt_paged_attention_bf16(const void* q, int64_t
     a.plan.least = 2;
     a.wp = wait_policy_from_env();
     a.device = dev;
+    if ((s = block_error_word(dev, &a.err)) != ARMT_OK) return s;
     a.part = static_cast<float*>(workspace);
     a.part_ml = reinterpret_cast<float2*>(a.part + (int64_t)shape.blocks * 2 * a.plan.rows * cache->head_dim);
     a.plans = reinterpret_cast<PlanRange*>(a.part_ml + (int64_t)shape.blocks * 4 * a.plan.rows);

@@ -17,6 +17,7 @@ struct PagedArgs {
   PlanRange* plans;  // [block]: what each block found for itself, for the joining kernel
   WaitPolicy wp;
   int device;
+  int* err;  // set by a bounded wait that gave up
 };
 
 // Untiled copy of n bytes (a multiple of 16, both ends 16-byte aligned).
@@ -87,6 +88,5 @@ cudaError_t launch_join(const PagedArgs& a, const PagedView& p, int head_dim, bo
 int tile_rows(int group);
 armt_status launch_tiles(const PagedArgs& a, const PagedView& p, const armt_kv_cache& cache, int n_q_heads,
                          cudaStream_t st);
-cudaError_t take_tiles_error(int* code);
 
 }  // namespace armt

@@ -76,8 +76,6 @@ __device__ __forceinline__ void take_registers() {
   if constexpr (!C::B16) asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(C::SOFTMAX_REGS));
 }
 
-__device__ int g_tiles_err;
-
 // Barriers, after the ring in shared memory.
 template <int RING, int RAW>
 struct TileBars {
@@ -161,7 +159,7 @@ __global__ void __launch_bounds__(TileCfg<HD, TYPE>::THREADS, 1)
   Bars& bar = *reinterpret_cast<Bars*>(raw + C::RAW_BYTES + C::BAD);
   static_assert(sizeof(Bars) <= 512 && sizeof(PlanScratch) <= C::BUF, "shared memory layout");
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  int* err = &g_tiles_err;
+  int* err = a.err;
   const uint64_t limit = a.wp.limit_ns;
 
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
@@ -762,13 +760,6 @@ armt_status launch_tiles(const PagedArgs& args, const PagedView& p, const armt_k
                                 : launch<128, ARMT_CACHE_BF16>(a, p, cache, n_q_heads, st);
   return cache.head_dim == 64 ? launch<64, ARMT_CACHE_E4M3>(a, p, cache, n_q_heads, st)
                               : launch<128, ARMT_CACHE_E4M3>(a, p, cache, n_q_heads, st);
-}
-
-cudaError_t take_tiles_error(int* code) {
-  cudaError_t e = cudaMemcpyFromSymbol(code, g_tiles_err, sizeof(int));
-  const int zero = 0;
-  if (e == cudaSuccess && *code != 0) e = cudaMemcpyToSymbol(g_tiles_err, &zero, sizeof(int));
-  return e;
 }
 
 }  // namespace armt
