@@ -303,8 +303,8 @@ ARMT_API armt_status armt_segment_attention_bf16(const void* qk, const void* vt,
  * current device since the last call, and clears it.  Their error word is a
  * device global of the library (one per device, looked up on the first call
  * with the device current); it stays set until read, and while it is set the
- * blocks' waits give up early, so their outputs are then undefined.  Allocates
- * nothing. */
+ * blocks' waits may give up early, so their outputs are then undefined.
+ * Allocates nothing. */
 ARMT_API armt_status armt_block_sync_status(void* stream);
 
 /* Fixed device scratch of armt_segment_attention_bf16_noalloc (bytes). */

@@ -21,7 +21,8 @@ namespace armt {
 
 void set_last_error(const std::string& msg);       // text returned by armt_last_error()
 armt_status ready_device(int* dev, int* num_sms);  // the current device, if the kernels run on it
-armt_status block_error_word(int dev, int** word); // what armt_block_sync_status reads and clears
+armt_status block_error_word(int dev, int** word);  // what armt_block_sync_status reads and clears
+void* current_context();
 
 bool encode_tmap_tiled3(CUtensorMap* map, const void* base, CUtensorMapDataType type, const cuuint64_t* dims,
                         const cuuint64_t* strides, const cuuint32_t* box, CUtensorMapSwizzle swizzle);

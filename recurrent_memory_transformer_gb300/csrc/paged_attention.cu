@@ -95,6 +95,9 @@ struct RowsCfg {
   static constexpr int SMEM = 1024 + STAGES * STAGE + JOIN + QUERIES;
 };
 
+// Set by a bounded wait that gave up; the joining kernel passes it on.
+__device__ int g_paged_err;
+
 // Barrier of the consumer warps.
 __device__ __forceinline__ void consumers_sync() { asm volatile("bar.sync 1, 128;" ::: "memory"); }
 
@@ -204,7 +207,7 @@ __device__ __forceinline__ void produce(const CUtensorMap& tm_k, const CUtensorM
                                         const PagedView& p, const PlanRange& range, RowsShared<C>& sh, uint8_t* smem) {
   constexpr bool B16 = C::B16;
   const int lane = threadIdx.x & 31;
-  int* err = a.err;
+  int* err = &g_paged_err;
   PlanCursor at = range.first;
   const int run = min(1 << p.page_shift, kKeys);  // keys of a tile that share a page
   const uint32_t run_bits = (1u << (run / 16)) - 1u;
@@ -289,7 +292,7 @@ __global__ void __launch_bounds__(kThreads + 32, RowsCfg<HD, TYPE, 0, WM>::BLOCK
   const int r = lane >> 2, c = lane & 3;
   const uint32_t sbase = smem_u32(smem);
   float* join = reinterpret_cast<float*>(smem + C::STAGES * C::STAGE);
-  int* err = a.err;
+  int* err = &g_paged_err;
 
   for (int i = tid; i < HD; i += kThreads + 32) bad[i] = Poison{0x7fffffff, 0x7fffffff, 0x7fffffff};
   init_barriers<C>(sh);
@@ -795,7 +798,7 @@ __global__ void __launch_bounds__(kThreads + 32, RowsCfg<HD, TYPE, NB>::BLOCKS)
   const uint32_t sbase = smem_u32(smem);
   float* join = reinterpret_cast<float*>(smem + C::STAGES * C::STAGE);
   uint2* queries = reinterpret_cast<uint2*>(smem + C::STAGES * C::STAGE + C::JOIN);  // [NB][KS][lane]
-  int* err = a.err;
+  int* err = &g_paged_err;
 
   for (int i = tid; i < HD; i += kThreads + 32) bad[i] = Poison{0x7fffffff, 0x7fffffff, 0x7fffffff};
   init_barriers<C>(sh);
@@ -1249,7 +1252,11 @@ __global__ void __launch_bounds__(256, TWO ? 3 : 4) join_kernel(const PagedArgs 
   // every block waits, also those with nothing to do: this kernel's end then
   // says that both have ended
   asm volatile("griddepcontrol.wait;" ::: "memory");
+  // the last block seldom has rows to join: its look at the error word delays nobody
+  if (blockIdx.x + 1 == gridDim.x && blockIdx.y == 0 && threadIdx.x == 0 && *a.own_err != 0)
+    atomicCAS(a.err, 0, atomicExch(a.own_err, 0));
   const int i = (int)blockIdx.x + 1;
+  if (i >= a.plan.blocks) return;
   const PlanRange range = a.plans[i];
   const PlanCursor prev = a.plans[i - 1].first;
   if (range.empty) return;
@@ -1456,9 +1463,8 @@ armt_status check_attention(const armt_kv_cache* cache, const armt_paged_batch* 
 }  // namespace
 
 cudaError_t launch_join(const PagedArgs& a, const PagedView& p, int head_dim, bool two, cudaStream_t st) {
-  if (a.plan.blocks < 2) return cudaSuccess;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)a.plan.blocks - 1, (unsigned)((a.plan.rows + kJoinRows - 1) / kJoinRows));
+  cfg.gridDim = dim3((unsigned)std::max(1, a.plan.blocks - 1), (unsigned)((a.plan.rows + kJoinRows - 1) / kJoinRows));
   cfg.blockDim = dim3(256);
   cfg.stream = st;
   cudaLaunchAttribute at[1];
@@ -1524,6 +1530,9 @@ extern "C" ARMT_API armt_status armt_paged_attention_bf16(const void* q, int64_t
     a.wp = wait_policy_from_env();
     a.device = dev;
     if ((s = block_error_word(dev, &a.err)) != ARMT_OK) return s;
+    static DeviceSymbol word;
+    const cudaError_t e = word.find(g_paged_err, dev, &a.own_err);
+    if (e != cudaSuccess) return launch_status(e, "paged attention set-up");
     a.part = static_cast<float*>(workspace);
     a.part_ml = reinterpret_cast<float2*>(a.part + (int64_t)shape.blocks * 2 * a.plan.rows * cache->head_dim);
     a.plans = reinterpret_cast<PlanRange*>(a.part_ml + (int64_t)shape.blocks * 4 * a.plan.rows);

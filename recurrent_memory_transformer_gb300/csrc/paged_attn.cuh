@@ -17,7 +17,28 @@ struct PagedArgs {
   PlanRange* plans;  // [block]: what each block found for itself, for the joining kernel
   WaitPolicy wp;
   int device;
-  int* err;  // set by a bounded wait that gave up
+  int* own_err;  // the kernel's own error word, and the building blocks', which
+  int* err;      // armt_block_sync_status reads: the joining kernel passes one on to the other
+};
+
+// A device global's address on each device, looked up when the device's context is
+// new (and without device work, which a capture would refuse).
+struct DeviceSymbol {
+  std::atomic<void*> ctx[64] = {};
+  std::atomic<int*> at[64] = {};
+  cudaError_t find(const int& symbol, int dev, int** out) {
+    if (dev < 0 || dev > 63) return cudaErrorInvalidDevice;
+    void* now = current_context();
+    *out = at[dev].load();
+    if (*out != nullptr && ctx[dev].load() == now) return cudaSuccess;
+    void* p = nullptr;
+    const cudaError_t e = cudaGetSymbolAddress(&p, symbol);
+    if (e != cudaSuccess) return e;
+    *out = static_cast<int*>(p);
+    at[dev].store(*out);
+    ctx[dev].store(now);
+    return cudaSuccess;
+  }
 };
 
 // Untiled copy of n bytes (a multiple of 16, both ends 16-byte aligned).

@@ -76,6 +76,12 @@ __device__ __forceinline__ void take_registers() {
   if constexpr (!C::B16) asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(C::SOFTMAX_REGS));
 }
 
+// Set by a bounded wait that gave up; the joining kernel passes it on.  (A word
+// of the module's own: a pointer among the arguments costs the softmax warps
+// registers that they spill, 2 x 1,024 rows over 16K 474 us -> 486, e4m3 head_dim
+// 64 485 -> 507.)
+__device__ int g_tiles_err;
+
 // Barriers, after the ring in shared memory.
 template <int RING, int RAW>
 struct TileBars {
@@ -159,7 +165,7 @@ __global__ void __launch_bounds__(TileCfg<HD, TYPE>::THREADS, 1)
   Bars& bar = *reinterpret_cast<Bars*>(raw + C::RAW_BYTES + C::BAD);
   static_assert(sizeof(Bars) <= 512 && sizeof(PlanScratch) <= C::BUF, "shared memory layout");
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  int* err = a.err;
+  int* err = &g_tiles_err;
   const uint64_t limit = a.wp.limit_ns;
 
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
@@ -510,7 +516,7 @@ __global__ void __launch_bounds__(TileCfg<HD, TYPE>::THREADS, 1)
             ok = agree(ok);
             if (!ok) break;
             if (!k && notes_hold_back(items, j, count)) {  // (in the meeting above: 232 us for 228, 32 x 10 rows)
-              ok = agree(notes_free());
+              ok = agree(__all_sync(0xffffffffu, notes_free()));
               if (!ok) break;
             }
             if (!k) clean(b, at.tile + j, tiles + j);
@@ -751,7 +757,10 @@ int tile_rows(int group) { return 2 * (128 / group) * group; }
 
 armt_status launch_tiles(const PagedArgs& args, const PagedView& p, const armt_kv_cache& cache, int n_q_heads,
                          cudaStream_t st) {
+  static DeviceSymbol word;
   PagedArgs a = args;
+  const cudaError_t e = word.find(g_tiles_err, a.device, &a.own_err);
+  if (e != cudaSuccess) return launch_status(e, "paged attention set-up");
   a.plan.keys = kKeys;
   a.plan.fixed = 5 * kKeys;  // an item's beginning and end take about as long as five tiles
   a.plan.least = 2;
