@@ -63,8 +63,8 @@ namespace {
 // exponential of its own, the weight is 2^(score - m + e), and the output is
 // sum / l * 2^(m - u).  The first exponents beyond are found where the reference
 // is about to move, and send the tile to the wide form, so that the others pay a
-// comparison and some registers (16 sequences to 8K: 62 us with 12 rows, 86 with
-// 28, 90 with 64 of head_dim 64; one reference for all, wrong beyond: 57, 85, 86;
+// comparison and some registers (16 sequences to 8K: 59 us with 12 rows, 83 with
+// 28, 88 with 64 of head_dim 64; one reference for all, wrong beyond: 56, 85, 86;
 // two exponentials for all: 62, 91, 104).
 
 constexpr int kKeys = 64;      // keys of a tile
@@ -83,7 +83,7 @@ struct RowsCfg {
   static constexpr int POOL = kKeys * ROW;
   static constexpr int SCALES = B16 ? 0 : 2 * kKeys;
   static constexpr int STAGE = (2 * POOL + SCALES + 1023) / 1024 * 1024;
-  // resident on an SM: registers, mostly (64 rows over codes: 90 us, 100 with three blocks, whose sums spill)
+  // resident on an SM: registers, mostly (64 rows over codes: 88 us, 100 with three blocks, whose sums spill)
   static constexpr int BLOCKS = (HD == 64 && (B16 || WM != 4)) || (NB == 1 && !B16) ? 3 : 2;
   static constexpr int JOIN = 2 * 32 * 32 * 4;  // two warps' pieces of 32 values a lane
   static constexpr int QUERIES = NB * HD * 16;  // turned: the queries' fragments
@@ -168,7 +168,9 @@ struct RowFactors {
   float first, second;
 };
 __device__ __forceinline__ RowFactors row_factors(float l, float m, float u) {
-  const float inv = weight_share(l, m);
+  // weight_share(l, m) with the hardware's reciprocal (2^-22 off), which spills
+  // less: 12 rows over codes 59 us for 61, 28 rows 83 for 86
+  const float inv = l == 0.f ? (m == -INFINITY ? 0.f : NAN) : __fdividef(1.f, l);
   const float half = m == u ? 1.f : fast_exp2(0.5f * (m - u));
   return RowFactors{inv * half, half};
 }
