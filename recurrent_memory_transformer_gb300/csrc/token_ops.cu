@@ -29,7 +29,7 @@ __device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.w
 // row into registers (RV groups of 4 values a thread), works with the slice's
 // own maximum m_c, and after the exchange scales by 2^((m_c - M) c) / S: one
 // read and one write of the row.  All in fp32; the exponentials are the hardware's
-// ex2 (2^-22), twice a value: 8e-8 to 1.3e-7 against 64 bits, a plain fp32 softmax
+// ex2 (2^-22), twice a value: 6e-8 to 2.2e-7 against 64 bits, a plain fp32 softmax
 // 3e-8 to 1e-7.
 
 constexpr int kProbThreads = 512;
